@@ -11,6 +11,9 @@ has not been built, or a tensor is not on a CUDA device, the call raises.
 ``scores`` is fp32 [B, row_stride] with unit inner stride (raw/paged) or a packed
 1-D buffer (ragged). Rows of ``out`` hold the selected positions, mapped, in an
 unspecified order, followed by -1 where a row has fewer than k positions.
+
+The operators that make such scores and read back what was selected (``indexer_*``:
+rotary positions, an e4m3 cache with block scales, the scores) are in ``indexer``.
 """
 
 from __future__ import annotations
@@ -30,6 +33,9 @@ __all__ = [
     "topk_set_cta_threads", "topk_guard_hits", "topk_reset_guard_hits",
     "topk_workspace_bytes", "topk_set_row_split", "topk_set_tie_capacity", "topk_set_fast_tier",
     "topk_set_staged_tier", "topk_set_chip_split",
+    "indexer_rotary", "indexer_rotary_freqs", "indexer_quantise", "indexer_cache_write",
+    "indexer_cache_read", "indexer_scores", "indexer_guard_hits", "indexer_reset_guard_hits",
+    "INDEXER_BLOCK", "INDEXER_MAX_HEADS",
 ]
 
 TOPK_MAX_K = 2048
@@ -103,6 +109,7 @@ def load_library() -> ctypes.CDLL:
             lib.topk_set_staged_tier.argtypes = [ctypes.c_int]
             lib.topk_set_chip_split.restype = ctypes.c_int
             lib.topk_set_chip_split.argtypes = [ctypes.c_int]
+            indexer.declare(lib)
             _lib = lib
     return _lib
 
@@ -432,3 +439,9 @@ def topk_set_staged_tier(mode: int) -> int:
     copied to shared memory from kernel start): 1 automatic (default), 2 always with
     the whole row staged, 3 always with half a row staged, 0 never."""
     return int(load_library().topk_set_staged_tier(int(mode)))
+
+
+from . import indexer  # noqa: E402  (it uses the loader and the checks above)
+from .indexer import (  # noqa: E402
+    INDEXER_BLOCK, INDEXER_MAX_HEADS, indexer_cache_read, indexer_cache_write, indexer_guard_hits,
+    indexer_quantise, indexer_reset_guard_hits, indexer_rotary, indexer_rotary_freqs, indexer_scores)

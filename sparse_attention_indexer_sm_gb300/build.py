@@ -19,13 +19,15 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libtopk_transform.so")
 
-SOURCES = ("topk_select.cu", "topk_api.cu")
+SOURCES = ("topk_select.cu", "topk_api.cu", "indexer_rotary.cu", "indexer_cache.cu",
+           "indexer_scores.cu")
 # The kernel source is compiled once per (CTA size, form) and once per CTA size for
 # the dispatch by form: ten objects that build in parallel.
 KERNEL_OBJECTS = [(f"topk_select_{cta}_{form}", ["-DTOPK_CTA_THREADS=%d" % cta, "-DTOPK_FORM=%d" % form])
                   for cta in (512, 256) for form in range(4)]
 KERNEL_OBJECTS += [(f"topk_select_{cta}", ["-DTOPK_CTA_THREADS=%d" % cta]) for cta in (512, 256)]
-HEADERS = (os.path.join(CSRC, "topk_select.cuh"), os.path.join(INCLUDE, "topk_transform.h"))
+HEADERS = (os.path.join(CSRC, "topk_select.cuh"), os.path.join(CSRC, "indexer_common.cuh"),
+           os.path.join(INCLUDE, "topk_transform.h"), os.path.join(INCLUDE, "indexer_ops.h"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I" + INCLUDE, "-I" + CSRC]
@@ -54,7 +56,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     exe = nvcc()
     procs, objs = [], []
     units = [(name, defs, "topk_select.cu") for name, defs in KERNEL_OBJECTS]
-    units.append(("topk_api", [], "topk_api.cu"))
+    units += [(os.path.splitext(src)[0], [], src) for src in SOURCES[1:]]
     for name, defs, src in units:
         obj = os.path.join(BUILD_DIR, name + ".o")
         cmd = [exe, *NVCC_FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]

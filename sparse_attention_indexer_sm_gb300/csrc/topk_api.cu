@@ -330,6 +330,10 @@ topk_problem_t problem(int32_t form, const float* scores, int64_t row_stride,
 
 }  // namespace
 
+namespace topk_gb300 {
+int record_cuda_error(cudaError_t e) { return fail_cuda(e); }
+}  // namespace topk_gb300
+
 extern "C" {
 
 size_t topk_workspace_bytes(int32_t batch, int64_t max_row_len, int32_t /*k*/) {
