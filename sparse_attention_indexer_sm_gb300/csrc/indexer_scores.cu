@@ -11,12 +11,18 @@
 // operations and is bound by memory; a prompt's chunk shares a key tile between the queries of a group
 // and is bound by the relu-sum of the epilogue and by the tensor cores, about evenly.
 //
-// One CTA an SM, persistent over (sequence, query group, chunk of tiles); its warps share out the work:
-//   warp 0      page ids and TMA copies: a ring of key tiles, two buffers of queries
-//   warp 1      tcgen05.mma
-//   warps 2, 3  the keys' scales into a ring, four tiles at once: they are a dependent load
-//               behind the page id, which no warp with other work should wait for
-//   warps 4-7, 8-11  two epilogue groups that take the tiles in turn
+// One CTA an SM, persistent over (sequence, query group, chunk of tiles). A tile's products are one unit of up
+// to 128 columns, or two (the same number for a whole launch). Its warps share out the work; a lone warp takes some 50 cycles for each barrier it
+// looks at, so that every role that a tile passes through has two warps or four, which take turns:
+//   warps 0, 1  page ids and TMA copies: a ring of key tiles, two buffers of queries
+//   warps 2, 3  tcgen05.mma, each for the units of one epilogue group
+//   warps 4-7   the keys' scales, two tiles at once: they are a dependent load behind the page id,
+//               which no warp with other work should wait for
+//   warps 8-11, 12-15  two epilogue groups that take the units in turn, each with a weight for every column
+//               in registers: from shared memory a weight costs as much as four columns' arithmetic
+// A barrier's parity tells a phase from the next one, but not from the one after that. So each place of a
+// ring belongs to the same warp of a role throughout: tiles and units are dealt out by their running
+// numbers over the whole launch, and the rings' lengths are multiples of the numbers of warps.
 // A page is copied in pieces of the largest power of two of rows that divides its size, so
 // every page size takes the same path.
 
@@ -31,16 +37,25 @@ namespace {
 
 constexpr int kDim = INDEXER_SCORE_DIM;  // bytes of a key's codes: one swizzled row
 constexpr int kTile = 128;               // keys of a tile: the rows of one MMA, the lanes of TMEM
-constexpr int kThreads = 384;
-constexpr int kMaxColumns = 256;         // N of one MMA
+constexpr int kThreads = 512;
+constexpr int kLoaders = 2, kScalers = 4;  // warps (and two for the MMAs)
+constexpr int kEpilogue = 8;               // first warp of the epilogue
+constexpr int kMaxColumns = 256;         // heads of a group's queries
+constexpr int kWarpColumns = 128;        // columns of a unit, N of its MMAs: a register each in the epilogue
+// Registers of a thread: 128 at launch, moved from the first eight warps to the epilogue
+// (512 * 128 = 256 * 64 + 256 * 192).
+constexpr int kFewRegisters = 64, kManyRegisters = 192;
 constexpr int kTmemColumns = 512;
 constexpr int kKeyStages = 8;
 constexpr int kMaxTmemStages = 8;
-constexpr int kScaleStages = 8;          // of each epilogue group
-constexpr int kScaleBatch = 4;
+constexpr int kScaleBatch = 2;
+static_assert(kKeyStages % kLoaders == 0 && kKeyStages % 2 == 0 && 4 % kScalers == 0 && kMaxTmemStages == 8, "a ring's place belongs to one warp of a role");
+constexpr int kMaxChunk = 64;            // tiles of an item
+constexpr int kItemCost = 4;             // tiles that the start of an item costs
 constexpr int kMaxGroup = 16;            // queries of a group
 constexpr int kEpilogueWarps = 8;
-constexpr int kWaitLimit = 1 << 20;      // tries of a wait before it is given up
+constexpr int kWaitLimit = 1 << 17;      // tries of a wait before it is given up,
+constexpr uint32_t kWaitNs = 20000;      // each of which may sleep this long: 2.6 s in all
 
 // A scale that stands for a page outside the cache; NaN scales of the cache get other bits.
 constexpr uint32_t kNoPage = 0x7fc00001u;
@@ -58,21 +73,23 @@ struct ScoresParams {
   int64_t num_pages, scale_ps, scale_ts, pt_stride;
   int64_t row_len, items, slices;  // slices: items of one chunk of tiles (sequences * groups)
   int32_t page_size, piece_rows;
+  uint32_t page_magic, page_shift; // row / page_size = (row * magic) >> (31 + shift) for rows below 2^31
+  int32_t quads;                   // pages hold whole quads of keys: 1; and their scales are aligned 16-byte quads: 2
   int32_t queries, heads, group, groups;
   int32_t tiles, chunk;            // tiles of a row; tiles of an item
-  int32_t tmem_stages, tmem_stride;
+  int32_t tmem_shift, tmem_stride; // 2^tmem_shift stages of tmem_stride columns
+  int32_t units, unit_queries;     // units of a tile (1 or 2); queries of a unit
 };
 
 struct Shared {
   alignas(1024) uint8_t keys[kKeyStages][kTile * kDim];
   alignas(1024) uint8_t queries[2][kMaxColumns * kDim];
-  alignas(16) float scales[2][kScaleStages][kTile];
-  alignas(16) float weights[kEpilogueWarps][kMaxColumns];  // each warp's own copy: no barrier among them
+  alignas(16) float scales[kMaxTmemStages][kTile];
+  alignas(16) float weights[kEpilogueWarps][kWarpColumns];  // each warp's own copy: no barrier among them
   int32_t lens[kEpilogueWarps][kMaxGroup];
   alignas(8) uint64_t key_full[kKeyStages], key_empty[kKeyStages];
   uint64_t query_full[2], query_empty[2];
   uint64_t tmem_full[kMaxTmemStages], tmem_empty[kMaxTmemStages];
-  uint64_t scale_full[2][kScaleStages], scale_empty[2][kScaleStages];
   uint64_t drained;
   uint32_t tmem_base;
   int32_t aborted;
@@ -96,29 +113,46 @@ __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
-// Waits for the end of a barrier's phase, for the whole warp. False when this or another wait of
-// the CTA ran out: then every role leaves its loop.
-__device__ __forceinline__ bool bar_wait(Shared& s, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_try(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "r"(kWaitNs)
+      : "memory");
+  return ok != 0u;
+}
+
+// Waits for the end of a barrier's phase. False when this wait or another of the CTA ran out.
+__device__ __forceinline__ bool bar_wait_thread(Shared& s, uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_addr(bar);
-  bool done = false;
   for (int i = 0; i < kWaitLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (ok != 0u) {
-      done = true;
-      break;
-    }
-    if ((i & 255) == 255 && *const_cast<volatile int32_t*>(&s.aborted) != 0) break;
+    if (bar_try(addr, parity)) return true;
+    if (*const_cast<volatile int32_t*>(&s.aborted) != 0) return false;
   }
-  if (__all_sync(0xffffffffu, done)) return true;
-  if ((threadIdx.x & 31) == 0 && atomicExch(&s.aborted, 1) == 0) atomicAdd(&g_guard_hits, 1u);
+  if (atomicExch(&s.aborted, 1) == 0) atomicAdd(&g_guard_hits, 1u);
   return false;
+}
+
+// The same for a whole warp that issues copies or MMAs: it goes on, or leaves its loop, as one.
+__device__ __forceinline__ bool bar_wait(Shared& s, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, bar_wait_thread(s, bar, parity));
+}
+
+// At the end of a role, whatever ended it: until its copies or MMAs have landed, some milliseconds at most.
+__device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < 256 && !bar_try(smem_addr(bar), parity); ++i) {
+  }
+  __syncwarp();
+}
+
+// A wait of the other roles, which go on in any case: after a wait that ran out they run through to their end
+// with wrong numbers (and the count in g_guard_hits), in bounds.
+__device__ __forceinline__ void bar_pass(Shared& s, uint64_t* bar, uint32_t parity) {
+  bar_wait_thread(s, bar, parity);
+  __syncwarp();
 }
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y,
@@ -129,17 +163,30 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, void* dst, u
       : "memory");
 }
 
-// K-major rows of 128 bytes, 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Descriptors of K-major rows of 128 bytes, 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t matrix_desc(uint32_t addr) { return ((addr & 0x3ffffu) >> 4) | (1u << 16); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0u;
 }
 
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The products of a tile's 128 dimensions, 32 at a time. a, b: low words of the operands' descriptors.
+__device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n.reg .pred p, q;\n.reg .b64 x, y;\n.reg .b32 u, v;\n"
+      "setp.ne.b32 p, 0, 0;\nsetp.eq.b32 q, 0, 0;\n"
+      "mov.b64 x, {%1, %4};\nmov.b64 y, {%2, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n"
+      "add.u32 u, %1, 2;\nadd.u32 v, %2, 2;\nmov.b64 x, {u, %4};\nmov.b64 y, {v, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, q;\n"
+      "add.u32 u, %1, 4;\nadd.u32 v, %2, 4;\nmov.b64 x, {u, %4};\nmov.b64 y, {v, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, q;\n"
+      "add.u32 u, %1, 6;\nadd.u32 v, %2, 6;\nmov.b64 x, {u, %4};\nmov.b64 y, {v, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, q;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
       : "memory");
 }
 
@@ -195,27 +242,35 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
   return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
+__device__ __forceinline__ uint32_t page_of(const ScoresParams& p, uint32_t row) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(row) * p.page_magic) >> 31 >> p.page_shift);
+}
+
 // One item: `count` queries from `query` on (rows of seq_lens and out, all of sequence b)
 // against tiles [first, end); tiles from `seen` on have no key that any of the queries sees.
 struct Item {
   int64_t query;
-  int32_t b, count, first, seen, end, longest;
+  int32_t b, count, first, seen, end, longest, shortest;
+  int32_t len;  // of this lane's query
 };
 
-__device__ __forceinline__ int32_t clamp_len(const ScoresParams& p, int32_t len) {
-  return static_cast<int32_t>(min(max(static_cast<int64_t>(len), int64_t(0)), p.row_len));
-}
-
-// Whole warps call this. Items are ordered with the chunk of tiles outermost, so that the CTAs work on
-// the same tiles of a sequence at about the same time and find them in L2.
+// An item's place, and the load of its lengths: asked for one item ahead. Items are ordered with the
+// chunk of tiles outermost, so that the CTAs work on the same tiles of a sequence at about the same time
+// and find them in L2.
 __device__ __forceinline__ Item item_at(const ScoresParams& p, int64_t index) {
-  Item it;
+  Item it = {};
+  if (index >= p.items) return it;
   const int64_t c = index / p.slices;
   const int64_t slice = index - c * p.slices;
   it.b = static_cast<int32_t>(slice / p.groups);
@@ -225,309 +280,361 @@ __device__ __forceinline__ Item item_at(const ScoresParams& p, int64_t index) {
   it.first = static_cast<int32_t>(c) * p.chunk;
   it.end = min(it.first + p.chunk, p.tiles);
   const int lane = threadIdx.x & 31;
-  const int32_t len = lane < it.count ? clamp_len(p, p.seq_lens[it.query + lane]) : 0;
-  it.longest = __reduce_max_sync(0xffffffffu, len);
-  it.seen = max(it.first, min(it.end, static_cast<int32_t>((static_cast<int64_t>(it.longest) + kTile - 1) / kTile)));
+  if (lane < it.count) it.len = p.seq_lens[it.query + lane];
   return it;
 }
 
+// The lengths' part of an item. Whole warps call this.
+__device__ __forceinline__ void item_ready(const ScoresParams& p, Item& it) {
+  it.len = static_cast<int32_t>(min(static_cast<int64_t>(max(it.len, 0)), p.row_len));
+  it.longest = __reduce_max_sync(0xffffffffu, it.len);
+  it.shortest = __reduce_min_sync(0xffffffffu, (threadIdx.x & 31) < it.count ? it.len : INT32_MAX);
+  const int32_t tiles = static_cast<int32_t>((static_cast<uint32_t>(it.longest) + kTile - 1) / kTile);
+  it.seen = max(it.first, min(it.end, tiles));
+}
+
+// The copies of every kLoaders-th tile. kPieces: copies of a tile that a lane may have to issue.
+template <int kPieces>
 __device__ __forceinline__ void load_keys(const ScoresParams& p, Shared& s, const CUtensorMap* key_map,
-                                          const CUtensorMap* query_map, int head_rows) {
+                                          const CUtensorMap* query_map, int head_rows, int turn) {
   const int lane = threadIdx.x & 31;
   const int pieces = kTile / p.piece_rows;
   const uint32_t piece_bytes = static_cast<uint32_t>(p.piece_rows) * kDim;
-  int64_t tile_count = 0, item_count = 0;
+  uint32_t tiles = 0, items = 0;  // so far
+  uint32_t next_own = turn;       // the running number of this warp's next tile
   bool ok = true;
+  Item next_item = item_at(p, blockIdx.x);
   for (int64_t i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
-    const Item it = item_at(p, i);
+    Item it = next_item;
+    item_ready(p, it);
+    next_item = item_at(p, i + gridDim.x);
     if (it.seen <= it.first) continue;
-    const int qb = static_cast<int>(item_count & 1);
-    ok = bar_wait(s, &s.query_empty[qb], static_cast<uint32_t>((item_count >> 1) & 1) ^ 1u);
-    if (!ok) break;
-    if (lane == 0) {
-      bar_expect(&s.query_full[qb], static_cast<uint32_t>(head_rows * p.group) * kDim);
-      tma_load_3d(query_map, s.queries[qb], &s.query_full[qb], 0, 0, static_cast<int>(it.query));
-    }
-    ++item_count;
-    const int32_t* table = p.page_table + static_cast<int64_t>(it.b) * p.pt_stride;
-    int32_t page[4], next[4];
-    auto pages_of = [&](int t, int32_t (&ids)[4]) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int piece = lane + 32 * k;
-        const int64_t row = static_cast<int64_t>(t) * kTile + piece * p.piece_rows;
-        ids[k] = t < it.seen && piece < pieces && row < it.longest
-                     ? table[static_cast<uint32_t>(row) / static_cast<uint32_t>(p.page_size)]
-                     : -1;
-      }
-    };
-    pages_of(it.first, next);
-    for (int t = it.first; t < it.seen; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) page[k] = next[k];
-      pages_of(t + 1, next);
-      const int st = static_cast<int>(tile_count % kKeyStages);
-      ok = bar_wait(s, &s.key_empty[st], static_cast<uint32_t>((tile_count / kKeyStages) & 1) ^ 1u);
+    if (turn == 0) {
+      const int at = items & 1;
+      ok = bar_wait(s, &s.query_empty[at], (items >> 1 & 1u) ^ 1u);
       if (!ok) break;
-      ++tile_count;
-      uint32_t bytes = 0;
+      if (lane == 0) {
+        bar_expect(&s.query_full[at], static_cast<uint32_t>(head_rows * p.group) * kDim);
+        tma_load_3d(query_map, s.queries[at], &s.query_full[at], 0, 0, static_cast<int>(it.query));
+      }
+      ++items;
+    }
+    const int32_t* table = p.page_table + static_cast<int64_t>(it.b) * p.pt_stride;
+    int32_t page[kPieces], off[kPieces], next_page[kPieces], next_off[kPieces];
+    auto pages_of = [&](int t) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        bytes += piece_bytes * __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && page[k] < p.num_pages));
-      if (lane == 0) bar_expect(&s.key_full[st], bytes);
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (page[k] < 0 || page[k] >= p.num_pages) continue;
+      for (int k = 0; k < kPieces; ++k) {
         const int piece = lane + 32 * k;
         const uint32_t row = static_cast<uint32_t>(t) * kTile + piece * p.piece_rows;
-        tma_load_3d(key_map, s.keys[st] + piece * piece_bytes, &s.key_full[st], 0,
-                    static_cast<int>(row % static_cast<uint32_t>(p.page_size)), page[k]);
+        next_page[k] = -1;
+        if (t < it.seen && piece < pieces && row < static_cast<uint32_t>(it.longest)) {
+          const uint32_t slot = page_of(p, row);
+          next_off[k] = static_cast<int32_t>(row - slot * p.page_size);
+          next_page[k] = table[slot];
+        }
       }
-      __syncwarp();
+    };
+    int t = it.first + static_cast<int>((turn - tiles) % kLoaders);
+    pages_of(t);
+    for (; t < it.seen; t += kLoaders) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) page[k] = next_page[k], off[k] = next_off[k];
+      pages_of(t + kLoaders);
+      uint32_t copies = 0;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        copies += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && page[k] < p.num_pages));
+      const uint32_t n = tiles + (t - it.first), at = n % kKeyStages;
+      ok = bar_wait(s, &s.key_empty[at], (n / kKeyStages & 1u) ^ 1u);
+      if (!ok) break;
+      uint64_t* full = &s.key_full[at];
+      next_own = n + kLoaders;
+      // the phase ends with this arrival and all bytes, in whatever order they come
+      if (lane == 0) bar_expect(full, copies * piece_bytes);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        if (page[k] >= 0 && page[k] < p.num_pages)
+          tma_load_3d(key_map, s.keys[at] + (lane + 32 * k) * piece_bytes, full, 0, off[k], page[k]);
+      }
     }
+    tiles += it.seen - it.first;
   }
-  // no copy outlives the CTA, whatever ended the loop
-  const int64_t tiles = tile_count < kKeyStages ? tile_count : kKeyStages, items = item_count < 2 ? item_count : 2;
-  for (int64_t k = 1; k <= tiles; ++k) {
-    const int64_t c = tile_count - k;
-    bar_wait(s, &s.key_full[c % kKeyStages], static_cast<uint32_t>((c / kKeyStages) & 1));
-  }
-  for (int64_t k = 1; k <= items; ++k) {
-    const int64_t c = item_count - k;
-    bar_wait(s, &s.query_full[c & 1], static_cast<uint32_t>((c >> 1) & 1));
-  }
+  // no copy outlives the CTA (a place that was never used has not ended a phase, which its other parity says it has)
+  for (uint32_t n = next_own; n < next_own + kKeyStages; n += kLoaders)
+    bar_drain(&s.key_full[n % kKeyStages], (n / kKeyStages & 1u) ^ 1u);
+  if (turn == 0)
+    for (uint32_t n = items; n < items + 2; ++n) bar_drain(&s.query_full[n & 1], (n >> 1 & 1u) ^ 1u);
 }
 
-__device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint32_t tmem, int head_rows) {
-  const int lane = threadIdx.x & 31;
-  int64_t tile_count = 0, item_count = 0;
-  int ts = 0;
-  uint32_t ts_phase = 0;
+// A warp's tiles of an item, where those of epilogue group `wg` are every one (two units a tile) or every second one
+// of the launch (one unit a tile).
+__device__ __forceinline__ int first_tile(const ScoresParams& p, const Item& it, int wg, uint32_t tiles) {
+  return it.first + (p.units == 1 ? static_cast<int>((wg ^ tiles) & 1u) : 0);
+}
+
+// The products of the units of epilogue group `wg`.
+__device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint32_t tmem, int head_rows, int wg) {
+  const uint32_t half = (1u << p.tmem_shift) / 2;  // the group's TMEM stages: wg, wg + 2, ...
+  uint32_t tiles = 0, items = 0, units = 0;        // so far; units: of this group
   bool ok = true;
+  Item next_item = item_at(p, blockIdx.x);
   for (int64_t i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
-    const Item it = item_at(p, i);
+    Item it = next_item;
+    item_ready(p, it);
+    next_item = item_at(p, i + gridDim.x);
     if (it.seen <= it.first) continue;
-    const int qb = static_cast<int>(item_count & 1);
-    ok = bar_wait(s, &s.query_full[qb], static_cast<uint32_t>((item_count >> 1) & 1));
-    if (!ok) break;
-    ++item_count;
+    ok = bar_wait(s, &s.query_full[items & 1], items >> 1 & 1u);
+    const int u = p.units == 2 ? wg : 0;
+    const int queries_here = min(it.count - u * p.unit_queries, p.unit_queries);  // none in the rest of a short group
     // fp32 accumulators, e4m3 operands, both K-major, M = 128
-    const uint32_t columns = static_cast<uint32_t>(it.count * head_rows);
-    const uint32_t idesc = (1u << 4) | ((columns >> 3) << 17) | ((kTile >> 4) << 24);
-    const uint64_t b = matrix_desc(smem_addr(s.queries[qb]));
-    for (int t = it.first; t < it.seen; ++t) {
-      const int st = static_cast<int>(tile_count % kKeyStages);
-      ok = bar_wait(s, &s.key_full[st], static_cast<uint32_t>((tile_count / kKeyStages) & 1)) &&
-           bar_wait(s, &s.tmem_empty[ts], ts_phase ^ 1u);
+    const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(queries_here * head_rows) >> 3) << 17) | ((kTile >> 4) << 24);
+    const uint32_t b = matrix_desc(smem_addr(s.queries[items & 1])) + u * (kWarpColumns * kDim / 16);
+    for (int t = first_tile(p, it, wg, tiles); ok && t < it.seen; t += 3 - p.units, ++units) {
+      const uint32_t n = tiles + (t - it.first), key = n % kKeyStages;
+      const uint32_t stage = wg + 2 * (units & (half - 1)), phase = (units >> (p.tmem_shift - 1)) & 1u;
+      // both barriers at once while neither has to be waited for
+      const bool keys_here = bar_try(smem_addr(&s.key_full[key]), n / kKeyStages & 1u);
+      const bool stage_free = bar_try(smem_addr(&s.tmem_empty[stage]), phase ^ 1u);
+      if (!__all_sync(0xffffffffu, keys_here && stage_free))
+        ok = bar_wait(s, &s.key_full[key], n / kKeyStages & 1u) && bar_wait(s, &s.tmem_empty[stage], phase ^ 1u);
       if (!ok) break;
-      ++tile_count;
       tmem_fence_after();
-      if (lane == 0) {
-        const uint64_t a = matrix_desc(smem_addr(s.keys[st]));
-        const uint32_t d = tmem + static_cast<uint32_t>(ts * p.tmem_stride);
-#pragma unroll
-        for (int k = 0; k < kDim / 32; ++k) mma_e4m3(d, a + k * 2, b + k * 2, idesc, k > 0 ? 1u : 0u);
-        mma_commit(&s.key_empty[st]);
-        mma_commit(&s.tmem_full[ts]);
-        if (t + 1 == it.seen) mma_commit(&s.query_empty[qb]);
+      const uint32_t a = matrix_desc(smem_addr(s.keys[key]));
+      if (elect_one()) {
+        if (queries_here > 0) mma_tile(tmem + stage * p.tmem_stride, a, b, idesc);
+        mma_commit(&s.tmem_full[stage]);
+        mma_commit(&s.key_empty[key]);
+        if (p.units == 1) bar_arrive(&s.key_empty[key]);  // for the other warp, which has no unit here
       }
       __syncwarp();
-      if (++ts == p.tmem_stages) {
-        ts = 0;
-        ts_phase ^= 1u;
-      }
     }
+    if (ok && elect_one()) mma_commit(&s.query_empty[items & 1]);
+    __syncwarp();
+    ++items;
+    tiles += it.seen - it.first;
   }
   // no MMA outlives the CTA
-  if (lane == 0) mma_commit(&s.drained);
+  if (elect_one()) mma_commit(&s.drained);
   __syncwarp();
-  bar_wait(s, &s.drained, 0u);
+  bar_drain(&s.drained, 0u);
 }
 
-// The scales of the tiles of epilogue group `wg` (every second one), kScaleBatch tiles at once: the
-// page ids of all of them, then the scales, so that each latency is met once in a batch.
-__device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, int wg) {
-  constexpr int kKeys = kTile / 32;  // keys of a lane
+// The scales of every kScalers-th unit, kScaleBatch of them at once: the page ids of all of them, then the
+// scales, so that each latency is met once in a batch. They go where their unit's products go, to a
+// place for each TMEM stage, and share its barriers. A lane brings four neighbouring keys;
+// kQuads: they lie on one page.
+template <bool kQuads>
+__device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, int turn) {
+  constexpr int kPages = kQuads ? 1 : 4;
   const int lane = threadIdx.x & 31;
-  int64_t index = blockIdx.x, tile_count = 0, stored = 0;
-  Item it = {};
-  int t = 0;
-  bool more = index < p.items;
-  if (more) {
-    it = item_at(p, index);
-    t = it.first;
-  }
-  while (more) {
-    uint32_t got[kScaleBatch][kKeys];
-    int32_t page[kScaleBatch][kKeys];
-    int tiles = 0;
+  const int step = kScalers / p.units;                  // tiles from one unit of this warp to its next
+  const uint32_t place = p.units == 1 ? turn : turn / 2;  // of this warp's tiles among `step`
+  uint32_t tiles = 0;
+  Item next_item = item_at(p, blockIdx.x);
+  for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x) {
+    Item it = next_item;
+    item_ready(p, it);
+    next_item = item_at(p, i + gridDim.x);
+    const int32_t* table = p.page_table + static_cast<int64_t>(it.b) * p.pt_stride;
+    for (int t = it.first + static_cast<int>((place - tiles) & (step - 1)); t < it.seen; t += kScaleBatch * step) {
+      int32_t page[kScaleBatch][kPages];
+      uint32_t off[kScaleBatch][kPages];
 #pragma unroll
-    for (int u = 0; u < kScaleBatch; ++u) {
-      // on to the next tile of this group
-      bool found = false;
-      while (more && !found) {
-        if (t >= it.seen) {
-          index += gridDim.x;
-          more = index < p.items;
-          if (more) {
-            it = item_at(p, index);
-            t = it.first;
+      for (int u = 0; u < kScaleBatch; ++u) {
+#pragma unroll
+        for (int k = 0; k < kPages; ++k) {
+          const int tile = t + u * step;
+          const uint32_t j = static_cast<uint32_t>(tile) * kTile + 4 * lane + k;
+          off[u][k] = 0xffffffffu;  // past the longest query: never used
+          if (tile < it.seen && j < static_cast<uint32_t>(it.longest)) {
+            const uint32_t slot = page_of(p, j);
+            off[u][k] = j - slot * p.page_size;
+            page[u][k] = table[slot];
           }
-          continue;
-        }
-        found = (tile_count & 1) == wg;
-        ++tile_count;
-        if (!found) ++t;
-      }
-#pragma unroll
-      for (int k = 0; k < kKeys; ++k) {
-        const uint32_t j = static_cast<uint32_t>(t) * kTile + k * 32 + lane;
-        const bool seen = found && j < static_cast<uint32_t>(it.longest);
-        // past the longest query: 0, and never used
-        got[u][k] = seen ? j % static_cast<uint32_t>(p.page_size) : 0xffffffffu;
-        page[u][k] = seen ? p.page_table[static_cast<int64_t>(it.b) * p.pt_stride +
-                                         j / static_cast<uint32_t>(p.page_size)]
-                          : 0;
-      }
-      if (found) {
-        ++tiles;
-        ++t;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kScaleBatch; ++u) {
-#pragma unroll
-      for (int k = 0; k < kKeys; ++k) {
-        const uint32_t off = got[u][k];
-        if (off == 0xffffffffu) {
-          got[u][k] = 0u;
-        } else if (page[u][k] < 0 || page[u][k] >= p.num_pages) {
-          got[u][k] = kNoPage;
-          atomicAdd(&g_guard_hits, 1u);
-        } else {
-          got[u][k] = __float_as_uint(p.scales[page[u][k] * p.scale_ps + off * p.scale_ts]);
         }
       }
-    }
+      uint32_t got[kScaleBatch][4];
 #pragma unroll
-    for (int u = 0; u < kScaleBatch; ++u) {
-      if (u >= tiles) break;
-      const int st = static_cast<int>(stored % kScaleStages);
-      if (!bar_wait(s, &s.scale_empty[wg][st], static_cast<uint32_t>((stored / kScaleStages) & 1) ^ 1u)) return;
-      ++stored;
+      for (int u = 0; u < kScaleBatch; ++u) {
 #pragma unroll
-      for (int k = 0; k < kKeys; ++k) {
-        const uint32_t v = got[u][k];
-        s.scales[wg][st][k * 32 + lane] =
-            __uint_as_float((v & 0x7fffffffu) > 0x7f800000u && v != kNoPage ? kNan : v);
+        for (int k = 0; k < kPages; ++k) {
+          const bool inside = off[u][k] != 0xffffffffu && page[u][k] >= 0 && page[u][k] < p.num_pages;
+          const float* src = p.scales + (inside ? page[u][k] * p.scale_ps + off[u][k] * p.scale_ts : 0);
+          if constexpr (kQuads) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) got[u][q] = kNoPage;
+            if (inside && p.quads == 2) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              got[u][0] = v.x, got[u][1] = v.y, got[u][2] = v.z, got[u][3] = v.w;
+            } else if (inside) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) got[u][q] = __float_as_uint(src[q * p.scale_ts]);
+            }
+          } else {
+            got[u][k] = kNoPage;
+            if (inside) got[u][k] = __float_as_uint(*src);
+          }
+          if (!inside && off[u][k] != 0xffffffffu) atomicAdd(&g_guard_hits, 1u);
+        }
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&s.scale_full[wg][st]);
+#pragma unroll
+      for (int u = 0; u < kScaleBatch; ++u) {
+        const int tile = t + u * step;
+        if (tile >= it.seen) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t v = got[u][q];
+          got[u][q] = (v & 0x7fffffffu) > 0x7f800000u && v != kNoPage ? kNan : v;
+        }
+        const uint32_t unit = (tiles + (tile - it.first)) * p.units + (p.units == 1 ? 0 : turn & 1);
+        const uint32_t at = unit & ((1u << p.tmem_shift) - 1);
+        bar_pass(s, &s.tmem_empty[at], (unit >> p.tmem_shift & 1u) ^ 1u);
+        *reinterpret_cast<uint4*>(&s.scales[at][4 * lane]) = make_uint4(got[u][0], got[u][1], got[u][2], got[u][3]);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s.tmem_full[at]);
+      }
     }
+    tiles += it.seen - it.first;
   }
 }
 
-// Adds weight * relu(product) of N columns to two pairs of sums.
-template <int N>
-__device__ __forceinline__ void add_heads(const float (&r)[N], const float* weights, uint64_t (&acc)[2]) {
-  const float4* w = reinterpret_cast<const float4*>(weights);
-#pragma unroll
-  for (int h = 0; h < N / 4; ++h) {
-    const float4 f = w[h];
-    acc[0] = fma2(pack2(fmaxf(r[4 * h], 0.0f), fmaxf(r[4 * h + 1], 0.0f)), pack2(f.x, f.y), acc[0]);
-    acc[1] = fma2(pack2(fmaxf(r[4 * h + 2], 0.0f), fmaxf(r[4 * h + 3], 0.0f)), pack2(f.z, f.w), acc[1]);
-  }
-}
+// What an epilogue warp knows of the tile it works on.
+struct Lane {
+  float* out;            // this key's score of the warp's first query
+  const int32_t* lens;   // of the warp's queries
+  uint64_t* tmem_empty;
+  int64_t row_len;
+  uint32_t tmem;
+  float scale;
+  int32_t j, columns;
+  bool whole, no_page;   // every query of the group sees every key of the tile; this key is on no page
+};
 
-// One epilogue warp: relu, weights and the sum over heads of its 32 lanes (keys), for the tiles of
-// group `wg`. kHeads: columns of a query.
-template <int kHeads>
-__device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_t tmem, int wg) {
-  constexpr int kHalf = kHeads <= 32 ? kHeads : 32;   // columns of a load
-  constexpr int kStep = kHeads <= 32 ? kHeads : 64;   // columns of a round: one load, or two
-  constexpr int kWeights = kMaxColumns / 32;          // weights that a lane brings
-  const int tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x / 32 - 4;
-  float* const weights = s.weights[warp];
-  int32_t* const lens = s.lens[warp];
-  const uint32_t lane_base = tmem + (static_cast<uint32_t>(tid & ~31) << 16);
-  const float minus_inf = __int_as_float(0xff800000);
-  float w[kWeights];
-  auto weights_of = [&](int64_t index) {
-    if (index >= p.items) return;
-    const int64_t slice = index % p.slices, b = slice / p.groups;
-    const int g0 = static_cast<int>(slice - b * p.groups) * p.group;
-    const float* src = p.weights + (b * p.queries + g0) * p.heads;
+// Columns from C * kLoad on, which are on their way to r: the next load is sent off before they are summed.
+template <int kHeads, int kLoad, int C>
+__device__ __forceinline__ void columns_from(const Lane& l, const float (&w)[kWarpColumns], float (&r)[kLoad],
+                                             uint64_t acc0, uint64_t acc1) {
+  tmem_wait<kLoad>(r);
+  auto add = [&]() {
 #pragma unroll
-    for (int k = 0; k < kWeights; ++k) {
-      const int g = (lane + 32 * k) / kHeads, h = (lane + 32 * k) % kHeads;
-      w[k] = g < p.group && g0 + g < p.queries && h < p.heads ? src[g * p.heads + h] : 0.0f;
+    for (int h = 0; h < kLoad / 4; ++h) {
+      constexpr int at = C * kLoad;
+      acc0 = fma2(pack2(fmaxf(r[4 * h], 0.0f), fmaxf(r[4 * h + 1], 0.0f)),
+                  pack2(w[at + 4 * h], w[at + 4 * h + 1]), acc0);
+      acc1 = fma2(pack2(fmaxf(r[4 * h + 2], 0.0f), fmaxf(r[4 * h + 3], 0.0f)),
+                  pack2(w[at + 4 * h + 2], w[at + 4 * h + 3]), acc1);
+    }
+    if constexpr ((C + 1) * kLoad % kHeads == 0) {
+      constexpr int g = C * kLoad / kHeads;
+      const float2 a = unpack2(add2(acc0, acc1));
+      const float y = (a.x + a.y) * l.scale;
+      float* const out = l.out + g * l.row_len;
+      if (l.whole) {
+        *out = l.no_page ? __int_as_float(0xff800000) : y;
+      } else if (l.j < l.row_len) {
+        *out = l.no_page || l.j >= l.lens[g] ? __int_as_float(0xff800000) : y;
+      }
+      acc0 = acc1 = 0;
     }
   };
-  weights_of(blockIdx.x);
-  int64_t tile_count = 0, taken = 0;
-  for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x) {
-    const Item it = item_at(p, i);
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kWeights; ++k) weights[lane + 32 * k] = w[k];
-    if (lane < it.count) lens[lane] = clamp_len(p, p.seq_lens[it.query + lane]);
-    __syncwarp();
-    weights_of(i + gridDim.x);  // on their way while this item is worked on
-    float* const out = p.out + it.query * p.row_len;
-    for (int t = it.first; t < it.seen; ++t, ++tile_count) {
-      if ((tile_count & 1) != wg) continue;
-      const int64_t j = static_cast<int64_t>(t) * kTile + tid;
-      const int ss = static_cast<int>(taken % kScaleStages);
-      if (!bar_wait(s, &s.scale_full[wg][ss], static_cast<uint32_t>((taken / kScaleStages) & 1))) return;
-      const float scale = s.scales[wg][ss][tid];
-      __syncwarp();
-      if (lane == 0) bar_arrive(&s.scale_empty[wg][ss]);
-      ++taken;
-      const int ts = static_cast<int>(tile_count % p.tmem_stages);
-      if (!bar_wait(s, &s.tmem_full[ts], static_cast<uint32_t>((tile_count / p.tmem_stages) & 1))) return;
-      tmem_fence_after();
-      const uint32_t at = lane_base + static_cast<uint32_t>(ts * p.tmem_stride);
-      const bool no_page = __float_as_uint(scale) == kNoPage;
-      const int columns = it.count * kHeads;
-      auto release = [&](int next) {  // every column of the tile is in registers: its stage is free
-        if (next < columns) return;
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&s.tmem_empty[ts]);
-      };
-      uint64_t acc[2] = {0, 0};
-      for (int c = 0; c < columns; c += kStep) {
-        float r0[kHalf];
-        tmem_load<kHalf>(at + c, r0);
-        tmem_wait<kHalf>(r0);
-        if constexpr (kStep > kHalf) {
-          float r1[kHalf];
-          tmem_load<kHalf>(at + c + kHalf, r1);
-          add_heads<kHalf>(r0, weights + c, acc);
-          tmem_wait<kHalf>(r1);
-          release(c + kStep);
-          add_heads<kHalf>(r1, weights + c + kHalf, acc);
-        } else {
-          release(c + kStep);
-          add_heads<kHalf>(r0, weights + c, acc);
-        }
-        if ((c + kStep) % kHeads == 0) {
-          const int g = c / kHeads;
-          const float2 a = unpack2(acc[0]), b = unpack2(acc[1]);
-          const float y = ((a.x + a.y) + (b.x + b.y)) * scale;
-          if (j < p.row_len) out[g * p.row_len + j] = j < lens[g] && !no_page ? y : minus_inf;
-          acc[0] = acc[1] = 0;
-        }
-      }
-    }
-    // tiles that no query of the group sees
-    for (int t = it.seen + wg; t < it.end; t += 2) {
-      const int64_t j = static_cast<int64_t>(t) * kTile + tid;
-      if (j < p.row_len)
-        for (int g = 0; g < it.count; ++g) out[g * p.row_len + j] = minus_inf;
+  if constexpr ((C + 1) * kLoad < kWarpColumns) {
+    if ((C + 1) * kLoad < l.columns) {
+      float next[kLoad];
+      tmem_load<kLoad>(l.tmem + (C + 1) * kLoad, next);
+      add();
+      columns_from<kHeads, kLoad, C + 1>(l, w, next, acc0, acc1);
+      return;
     }
   }
+  // every column of the tile is in registers: its stage is free
+  tmem_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(l.tmem_empty);
+  add();
+}
+
+// One epilogue warp: relu, weights and the sum over heads of its 32 lanes (keys), for every second unit.
+// kHeads: columns of a query.
+template <int kHeads>
+__device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_t tmem, int wg) {
+  constexpr int kLoad = 16;                         // columns of a load
+  constexpr int kQueries = kWarpColumns / kHeads;   // queries of a unit at most
+  constexpr int kBring = kWarpColumns / 32;         // weights that a lane brings
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x / 32 - kEpilogue;
+  const float minus_inf = __int_as_float(0xff800000);
+  const int first = p.units == 2 ? wg * kQueries : 0;  // of this warp's queries in a group
+  float bring[kBring];
+  auto weights_of = [&](const Item& it) {
+    const float* src = p.weights + (it.query + first) * p.heads;
+#pragma unroll
+    for (int k = 0; k < kBring; ++k) {
+      const int g = (lane + 32 * k) / kHeads, h = (lane + 32 * k) % kHeads;
+      bring[k] = first + g < it.count && h < p.heads ? src[g * p.heads + h] : 0.0f;
+    }
+  };
+  Lane l;
+  l.row_len = p.row_len;
+  const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(tid & ~31) << 16);
+  const uint32_t half = (1u << p.tmem_shift) / 2;  // the group's TMEM stages: wg, wg + 2, ...
+  uint32_t tiles = 0, units = 0;                   // so far; units: of this group
+  Item next_item = item_at(p, blockIdx.x);
+  weights_of(next_item);
+  for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x) {
+    Item it = next_item;
+    item_ready(p, it);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kBring; ++k) s.weights[warp][lane + 32 * k] = bring[k];
+    if (lane < it.count) s.lens[warp][lane] = it.len;
+    __syncwarp();
+    float w[kWarpColumns];
+#pragma unroll
+    for (int k = 0; k < kWarpColumns / 4; ++k) {
+      const float4 f = reinterpret_cast<const float4*>(s.weights[warp])[k];
+      w[4 * k] = f.x, w[4 * k + 1] = f.y, w[4 * k + 2] = f.z, w[4 * k + 3] = f.w;
+    }
+    const int count = min(max(it.count - first, 0), kQueries);
+    l.columns = count * kHeads;
+    l.lens = s.lens[warp] + first;
+    float* const out = p.out + (it.query + first) * p.row_len;
+    next_item = item_at(p, i + gridDim.x);
+    weights_of(next_item);  // on their way while this item is worked on
+    for (int t = first_tile(p, it, wg, tiles); t < it.seen; t += 3 - p.units, ++units) {
+      const uint32_t stage = wg + 2 * (units & (half - 1));
+      l.tmem_empty = &s.tmem_empty[stage];
+      l.tmem = tmem_lane + stage * p.tmem_stride;
+      bar_pass(s, &s.tmem_full[stage], (units >> (p.tmem_shift - 1)) & 1u);
+      tmem_fence_after();
+      if (count == 0) {
+        if (lane == 0) bar_arrive(l.tmem_empty);
+        continue;
+      }
+      float r[kLoad];
+      tmem_load<kLoad>(l.tmem, r);
+      l.scale = s.scales[stage][tid];
+      l.j = t * kTile + tid;
+      l.out = out + l.j;
+      l.whole = t * kTile <= it.shortest - kTile;
+      l.no_page = __float_as_uint(l.scale) == kNoPage;
+      columns_from<kHeads, kLoad, 0>(l, w, r, 0, 0);
+    }
+    tiles += it.seen - it.first;
+    // tiles that no query of the group sees
+    for (int t = it.seen + (p.units == 2 ? 0 : wg); t < it.end; t += p.units == 2 ? 1 : 2) {
+      const int64_t j = static_cast<int64_t>(t) * kTile + tid;
+      if (j < p.row_len)
+        for (int g = 0; g < count; ++g) out[g * p.row_len + j] = minus_inf;
+    }
+  }
+}
+
+template <int kRegisters>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+template <int kRegisters>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
 }
 
 // kHeads: heads rounded up to 16, 32, 64 or 128. The rounding's rows of B are zeros (beyond the
@@ -542,21 +649,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKeyStages; ++i) {
       bar_init(&s.key_full[i], 1);
-      bar_init(&s.key_empty[i], 1);
+      bar_init(&s.key_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&s.query_full[i], 1);
-      bar_init(&s.query_empty[i], 1);
-      for (int k = 0; k < kScaleStages; ++k) {
-        bar_init(&s.scale_full[i][k], 1);
-        bar_init(&s.scale_empty[i][k], 4);
-      }
+      bar_init(&s.query_empty[i], 2);
     }
     for (int i = 0; i < kMaxTmemStages; ++i) {
-      bar_init(&s.tmem_full[i], 1);
+      bar_init(&s.tmem_full[i], 2);  // the products and the scales
       bar_init(&s.tmem_empty[i], 4);
     }
-    bar_init(&s.drained, 1);
+    bar_init(&s.drained, 2);
     s.aborted = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -573,10 +676,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   begin_after_prior_grids();
 
-  if (warp == 0) load_keys(p, s, &key_map, &query_map, kHeads);
-  else if (warp == 1) multiply(p, s, tmem, kHeads);
-  else if (warp < 4) load_scales(p, s, warp - 2);
-  else reduce<kHeads>(p, s, tmem, (warp - 4) / 4);
+  if (warp < kEpilogue) {
+    fewer_registers<kFewRegisters>();
+    if (warp < kLoaders && p.piece_rows >= 4) load_keys<1>(p, s, &key_map, &query_map, kHeads, warp);
+    else if (warp < kLoaders) load_keys<4>(p, s, &key_map, &query_map, kHeads, warp);
+    else if (warp < kLoaders + 2) multiply(p, s, tmem, kHeads, warp - kLoaders);
+    else if (p.quads != 0) load_scales<true>(p, s, warp - kLoaders - 2);
+    else load_scales<false>(p, s, warp - kLoaders - 2);
+  } else {
+    more_registers<kManyRegisters>();
+    reduce<kHeads>(p, s, tmem, (warp - kEpilogue) / 4);
+  }
 
   tmem_fence_before();
   __syncthreads();
@@ -691,21 +801,30 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   p.page_size = cache->page_size;
   p.piece_rows = cache->page_size & -cache->page_size;
   if (p.piece_rows > kTile) p.piece_rows = kTile;
+  while ((int64_t(1) << p.page_shift) < p.page_size) ++p.page_shift;
+  p.page_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + p.page_shift)) + p.page_size - 1) / p.page_size);
+  p.quads = p.page_size % 4 != 0 ? 0
+            : p.scale_ts == 1 && p.scale_ps % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0 ? 2 : 1;
   p.queries = queries;
   p.heads = heads;
   const int head_rows = heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
   p.group = kMaxColumns / head_rows < queries ? kMaxColumns / head_rows : queries;
   p.groups = (queries + p.group - 1) / p.group;
   p.tiles = static_cast<int32_t>((row_len + kTile - 1) / kTile);
-  // Tensor-memory stages of 32 columns or a larger power of two.
+  p.unit_queries = kWarpColumns / head_rows;
+  p.units = p.group > p.unit_queries ? 2 : 1;
+  // TMEM stages of 32 columns or a larger power of two: 4 or 8 of them
   p.tmem_stride = 32;
-  while (p.tmem_stride < p.group * head_rows) p.tmem_stride *= 2;
-  p.tmem_stages = kTmemColumns / p.tmem_stride < kMaxTmemStages ? kTmemColumns / p.tmem_stride : kMaxTmemStages;
-  // Tiles of an item: one while there are fewer tiles than SMs; otherwise so many that each SM gets
-  // 16 items or more (its share of uneven items evens out), 32 tiles at most.
+  while (p.tmem_stride < kWarpColumns && p.tmem_stride < p.group * head_rows) p.tmem_stride *= 2;
+  p.tmem_shift = p.tmem_stride == kWarpColumns ? 2 : 3;
+  // Tiles of an item: what takes the SM with the most items the least time when every row is full, an
+  // item's start counted as kItemCost tiles.
   p.slices = static_cast<int64_t>(batch) * p.groups;
-  const int64_t chunk = p.slices * p.tiles / (int64_t(sms) * 16);
-  p.chunk = static_cast<int32_t>(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk);
+  int64_t best = INT64_MAX;
+  for (int32_t chunk = 1; chunk <= kMaxChunk && chunk <= p.tiles; ++chunk) {
+    const int64_t items = p.slices * ((p.tiles + chunk - 1) / chunk), cost = (items + sms - 1) / sms * (chunk + kItemCost);
+    if (cost < best) best = cost, p.chunk = chunk;
+  }
   p.items = p.slices * ((p.tiles + p.chunk - 1) / p.chunk);
 
   CUtensorMap key_map, query_map;

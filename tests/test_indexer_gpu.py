@@ -523,6 +523,24 @@ def test_scores(fw, case):
     check_scores(fw.indexer_scores(*args), *args)
 
 
+@pytest.mark.parametrize("case", [(400, 1, 64, 300, 64), (90, 5, 64, 1000, 64), (70, 3, 128, 700, 64), (30, 50, 32, 600, 64),
+                                  (200, 2, 24, 900, 16), (3, 1, 64, 40000, 64)])
+def test_scores_of_many_rows(fw, case):
+    """More work than the chip holds at once, rows of every length among it (empty ones too), checked against
+    the same rows scored a few at a time, and some of them against the reference."""
+    q, w, codes, scales, table, lens, n = scores_inputs(sum(case), *case)
+    got = fw.indexer_scores(q, w, codes, scales, table, lens, n)
+    queries = case[1]
+    for b in range(0, case[0], max(1, case[0] // 9)):
+        part = q[b:b + 1], w[b:b + 1], codes, scales, table[b:b + 1], lens[b:b + 1], n
+        few = fw.indexer_scores(*part)
+        assert torch.equal(got[b * queries:(b + 1) * queries], few)
+        if b % 2 == 0:
+            check_scores(few, *part)
+    for _ in range(3):
+        assert torch.equal(fw.indexer_scores(q, w, codes, scales, table, lens, n), got)
+
+
 def test_scores_of_every_length(fw):
     """No keys, one key, both sides of every border of pages and tiles, past the row, negative."""
     lens = [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 192, 255, 256, 257, 383, 384, 385, 399, 400, 401, 2**31 - 1,
