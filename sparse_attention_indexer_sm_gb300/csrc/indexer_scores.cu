@@ -103,9 +103,10 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
 }
 
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void bar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) { bar_arrive(smem_addr(bar)); }
 
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
@@ -125,9 +126,20 @@ __device__ __forceinline__ bool bar_try(uint32_t addr, uint32_t parity) {
   return ok != 0u;
 }
 
+__device__ __forceinline__ bool bar_test(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // Waits for the end of a barrier's phase. False when this wait or another of the CTA ran out.
-__device__ __forceinline__ bool bar_wait_thread(Shared& s, uint64_t* bar, uint32_t parity) {
-  const uint32_t addr = smem_addr(bar);
+__device__ __forceinline__ bool bar_wait_thread(Shared& s, uint32_t addr, uint32_t parity) {
   for (int i = 0; i < kWaitLimit; ++i) {
     if (bar_try(addr, parity)) return true;
     if (*const_cast<volatile int32_t*>(&s.aborted) != 0) return false;
@@ -138,7 +150,7 @@ __device__ __forceinline__ bool bar_wait_thread(Shared& s, uint64_t* bar, uint32
 
 // The same for a whole warp that issues copies or MMAs: it goes on, or leaves its loop, as one.
 __device__ __forceinline__ bool bar_wait(Shared& s, uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, bar_wait_thread(s, bar, parity));
+  return __all_sync(0xffffffffu, bar_wait_thread(s, smem_addr(bar), parity));
 }
 
 // At the end of a role, whatever ended it: until its copies or MMAs have landed, some milliseconds at most.
@@ -150,8 +162,8 @@ __device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity) {
 
 // A wait of the other roles, which go on in any case: after a wait that ran out they run through to their end
 // with wrong numbers (and the count in g_guard_hits), in bounds.
-__device__ __forceinline__ void bar_pass(Shared& s, uint64_t* bar, uint32_t parity) {
-  bar_wait_thread(s, bar, parity);
+__device__ __forceinline__ void bar_pass(Shared& s, uint32_t addr, uint32_t parity) {
+  bar_wait_thread(s, addr, parity);
   __syncwarp();
 }
 
@@ -488,7 +500,7 @@ __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, in
         }
         const uint32_t unit = (tiles + (tile - it.first)) * p.units + (p.units == 1 ? 0 : turn & 1);
         const uint32_t at = unit & ((1u << p.tmem_shift) - 1);
-        bar_pass(s, &s.tmem_empty[at], (unit >> p.tmem_shift & 1u) ^ 1u);
+        bar_pass(s, smem_addr(&s.tmem_empty[at]), (unit >> p.tmem_shift & 1u) ^ 1u);
         *reinterpret_cast<uint4*>(&s.scales[at][4 * lane]) = make_uint4(got[u][0], got[u][1], got[u][2], got[u][3]);
         __syncwarp();
         if (lane == 0) bar_arrive(&s.tmem_full[at]);
@@ -502,8 +514,8 @@ __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, in
 struct Lane {
   float* out;            // this key's score of the warp's first query
   const int32_t* lens;   // of the warp's queries
-  uint64_t* tmem_empty;
   int64_t row_len;
+  uint32_t tmem_empty, next_full, next_phase;  // barriers: to be told that the tile is read; of the next unit
   uint32_t tmem;
   float scale;
   int32_t j, columns;
@@ -511,8 +523,9 @@ struct Lane {
 };
 
 // Columns from C * kLoad on, which are on their way to r: the next load is sent off before they are summed.
+// Whether the next unit is there already: asked before the last sums, for use after them.
 template <int kHeads, int kLoad, int C>
-__device__ __forceinline__ void columns_from(const Lane& l, const float (&w)[kWarpColumns], float (&r)[kLoad],
+__device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kWarpColumns], float (&r)[kLoad],
                                              uint64_t acc0, uint64_t acc1) {
   tmem_wait<kLoad>(r);
   auto add = [&]() {
@@ -542,15 +555,16 @@ __device__ __forceinline__ void columns_from(const Lane& l, const float (&w)[kWa
       float next[kLoad];
       tmem_load<kLoad>(l.tmem + (C + 1) * kLoad, next);
       add();
-      columns_from<kHeads, kLoad, C + 1>(l, w, next, acc0, acc1);
-      return;
+      return columns_from<kHeads, kLoad, C + 1>(l, w, next, acc0, acc1);
     }
   }
   // every column of the tile is in registers: its stage is free
   tmem_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) bar_arrive(l.tmem_empty);
+  const bool ready = bar_test(l.next_full, l.next_phase);
   add();
+  return ready;
 }
 
 // One epilogue warp: relu, weights and the sum over heads of its 32 lanes (keys), for every second unit.
@@ -575,8 +589,10 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
   Lane l;
   l.row_len = p.row_len;
   const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(tid & ~31) << 16);
-  const uint32_t half = (1u << p.tmem_shift) / 2;  // the group's TMEM stages: wg, wg + 2, ...
-  uint32_t tiles = 0, units = 0;                   // so far; units: of this group
+  const uint32_t stages = 1u << p.tmem_shift;      // the group's own: wg, wg + 2, ...
+  const uint32_t full_base = smem_addr(s.tmem_full), empty_base = smem_addr(s.tmem_empty);
+  uint32_t tiles = 0, stage = wg, phase = 0;
+  bool ready = false;
   Item next_item = item_at(p, blockIdx.x);
   weights_of(next_item);
   for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x) {
@@ -599,24 +615,33 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     float* const out = p.out + (it.query + first) * p.row_len;
     next_item = item_at(p, i + gridDim.x);
     weights_of(next_item);  // on their way while this item is worked on
-    for (int t = first_tile(p, it, wg, tiles); t < it.seen; t += 3 - p.units, ++units) {
-      const uint32_t stage = wg + 2 * (units & (half - 1));
-      l.tmem_empty = &s.tmem_empty[stage];
-      l.tmem = tmem_lane + stage * p.tmem_stride;
-      bar_pass(s, &s.tmem_full[stage], (units >> (p.tmem_shift - 1)) & 1u);
+    const int step = 3 - p.units;
+    for (int t = first_tile(p, it, wg, tiles); t < it.seen; t += step) {
+      const uint32_t at = stage, full = full_base + 8 * stage;
+      l.tmem_empty = empty_base + 8 * stage;
+      if (!ready) bar_pass(s, full, phase);
       tmem_fence_after();
+      stage += 2;
+      if (stage >= stages) {
+        stage = wg;
+        phase ^= 1u;
+      }
+      ready = false;
       if (count == 0) {
         if (lane == 0) bar_arrive(l.tmem_empty);
         continue;
       }
+      l.tmem = tmem_lane + at * p.tmem_stride;
       float r[kLoad];
       tmem_load<kLoad>(l.tmem, r);
-      l.scale = s.scales[stage][tid];
+      l.scale = s.scales[at][tid];
       l.j = t * kTile + tid;
       l.out = out + l.j;
       l.whole = t * kTile <= it.shortest - kTile;
       l.no_page = __float_as_uint(l.scale) == kNoPage;
-      columns_from<kHeads, kLoad, 0>(l, w, r, 0, 0);
+      l.next_full = full_base + 8 * stage;
+      l.next_phase = phase;
+      ready = __all_sync(0xffffffffu, columns_from<kHeads, kLoad, 0>(l, w, r, 0, 0));
     }
     tiles += it.seen - it.first;
     // tiles that no query of the group sees
