@@ -17,7 +17,8 @@
  *
  * Memory and ownership, stream order, errors: as in topk_transform.h. Every pointer
  * is device memory owned by the caller; the library never allocates, frees or
- * synchronises; a call enqueues one kernel on `stream` and returns. Every launch
+ * synchronises; a call enqueues one kernel on `stream` (several where it has 2^30 parts of
+ * rows or more) and returns. Every launch
  * allows programmatic dependent launch and waits for the previous kernel of the
  * stream before it touches memory. Host-checkable problems return a status and
  * launch nothing. Values in device memory cannot be checked by the host: a slot or a

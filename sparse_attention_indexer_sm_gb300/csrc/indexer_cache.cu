@@ -1,16 +1,22 @@
 // Rows to e4m3 with a scale for each block of 128 columns: on their own, or written into
 // a paged cache; and cache rows back in 16 or 32 bits.
 //
-// Bound by memory: each element is read once and written once.
-// - Rounding. A code is the e4m3 value nearest to the real quotient x / scale. The fp32
-//   quotient alone may have been rounded onto (or across) the middle between two codes, so
-//   its remainder, which one fma gives exactly, is kept as a sticky last bit: the quotient
-//   rounded to odd, which then rounds to e4m3 as the real one does. With a power of two as
-//   the scale the quotient is exact already.
-// - The split. Half a warp owns a block: 16 lanes of 8 values, the largest magnitude found
-//   by four shuffles on the bit patterns, as integers, which order a NaN above everything.
+// Bound by memory: each element is read once and written once, so few operations may be spent on one.
+// - Rounding. A code is the e4m3 value nearest to the real quotient x / scale. x times an approximate
+//   1 / scale, a little too small and a little too large, gives two codes with one instruction for
+//   each pair; where they agree, the code is that, and almost everywhere they do. A lane in which one
+//   pair differs takes each value's remainder, which one fma gives exactly, as a sticky last bit: the
+//   quotient rounded to odd, which rounds to e4m3 as the real one does. With a power of two as the
+//   scale the quotient is exact already.
+// - The split. Eight lanes own a block, 16 values each, two blocks in flight in each lane: with sixteen lanes of 8
+//   values what a lane does once a block (its place, its scale) cost as much as its values, and the kernel
+//   was bound by instructions (8192 x 64 rows of 128 in bf16: 60 us). The largest magnitude is
+//   found on the bit patterns, as integers, which order a NaN above everything. Reading back, a lane
+//   makes one 32-byte store of 16 or 8 columns, four rows in flight.
 
 #include <cuda_fp8.h>
+
+#include <cstring>
 
 #include "indexer_common.cuh"
 
@@ -18,10 +24,14 @@ namespace indexer_gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlockLanes = 16;                     // lanes of one block
-constexpr int kLaneValues = INDEXER_BLOCK / kBlockLanes;  // values of one lane: 8
+constexpr int kBlockLanes = 8;                            // lanes of one block
+constexpr int kLaneValues = INDEXER_BLOCK / kBlockLanes;  // values of one lane: 16, in two pieces of 8 columns
+constexpr int kPiece = 8;
+constexpr int kPieces = kLaneValues / kPiece;
+constexpr int kBlocksAhead = 2;                           // blocks that a lane has in flight
 constexpr uint32_t kAmaxFloorBits = (127u - 64u) << 23;   // 2^-64
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr int kRounds = 4;                                // cache rows that a lane has in flight
 
 // Slots outside the cache that were met (see indexer_guard_hits).
 __device__ unsigned int g_guard_hits;
@@ -34,9 +44,10 @@ struct QuantParams {
   const float* weights;   // nullptr: scales as they are
   int64_t x_ts, x_hs;
   int64_t code_ps, code_ts, scale_ps, scale_ts;
-  int64_t units;          // rows * blocks of a row
-  int64_t capacity;       // slots of the cache
-  int32_t heads, dim, blocks, page_size, pow2;
+  uint32_t units;         // rows * blocks of a row
+  uint32_t capacity;      // slots of the cache
+  Divisor heads, blocks, page_size;
+  int32_t dim, pow2;
 };
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -59,97 +70,175 @@ __device__ __forceinline__ float quotient_to_odd(float x, float scale, float inv
   return __uint_as_float(bits);
 }
 
-// VEC: a lane's values are 8 consecutive columns, loaded 16 bytes at a time and stored as 8
-// bytes; otherwise columns lane, lane + 16, ... one by one.
-template <typename T, bool VEC>
+// top / 448, correctly rounded (Markstein: a quotient from the correctly rounded reciprocal, corrected once by its
+// exact remainder).
+__device__ __forceinline__ float over_448(float top) {
+  const float y = 1.0f / 448.0f, q = top * y;
+  return fmaf(fmaf(-448.0f, q, top), y, q);
+}
+
+// 1 / scale to within a step: scales lie between 2^-73 and 2^120.
+__device__ __forceinline__ float about_inverse(float scale) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+  return r;
+}
+
+// The bit pattern of the largest magnitude among a block's values, NaN above everything, as fp32.
+template <typename T>
+__device__ __forceinline__ uint32_t block_top(const uint32_t (&bits)[kLaneValues * sizeof(T) / 4]) {
+  constexpr int kWords = kLaneValues * sizeof(T) / 4;
+  constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kWords; i += 2) {  // pairs of 16 bits order as integers too
+    const uint32_t a = bits[i] & kAbs, b = bits[i + 1] & kAbs;
+    if constexpr (sizeof(T) == 4) top = __vimax3_u32(top, a, b);
+    else top = __vimax3_u16x2(top, a, b);
+  }
+#pragma unroll
+  for (int d = kBlockLanes / 2; d > 0; d /= 2) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, d);
+    if constexpr (sizeof(T) == 4) top = max(top, other);
+    else top = __vmaxu2(top, other);
+  }
+  if constexpr (sizeof(T) == 4) {
+    return top;
+  } else {
+    const unsigned short raw = static_cast<unsigned short>(max(top & 0xffffu, top >> 16));
+    T v;
+    memcpy(&v, &raw, 2);
+    return __float_as_uint(to_float(v));
+  }
+}
+
+// Codes of two values, as 16 bits, from their products with a number near 1 / scale.
+__device__ __forceinline__ uint32_t codes_of(const float* v, float inv) { return e4m3x2(v[0] * inv, v[1] * inv); }
+
+// VEC: a lane's pieces are 8 consecutive columns each, loaded 16 bytes at a time and stored as 8
+// bytes; otherwise its columns are lane, lane + 8, ... one by one. SLOTS: row r goes to slots[r].
+template <typename T, bool VEC, bool SLOTS>
 __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p) {
+  constexpr int kWords = kLaneValues * sizeof(T) / 4, kPieceWords = kWords / kPieces;
   begin_after_prior_grids();
   const int lane = threadIdx.x % kBlockLanes;
   const T* x = static_cast<const T*>(p.x);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / kBlockLanes);
-  // both halves of a warp run the same number of rounds (the shuffles name the whole warp)
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kBlockLanes;
-  for (int64_t u0 = first & ~int64_t(1); u0 < p.units; u0 += stride) {
-    const int64_t u = u0 + (first & 1);
-    const bool live = u < p.units;
-    const int64_t row = live ? u / p.blocks : 0;
-    const int kb = live ? static_cast<int>(u - row * p.blocks) : 0;
-    const int64_t t = row / p.heads;
-    const T* src = x + t * p.x_ts + (row - t * p.heads) * p.x_hs + kb * INDEXER_BLOCK;
-    const int cols = live ? min(p.dim - kb * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
-    float v[kLaneValues];
-    if constexpr (VEC) {
-      constexpr int kV = 16 / sizeof(T);
-      if (lane * kLaneValues < cols) {
+  // a group of lanes takes kBlocksAhead consecutive blocks a round; all groups of a warp run the same number of
+  // rounds (the shuffles name the whole warp)
+  constexpr uint32_t kGroups = 32 / kBlockLanes;
+  const uint32_t group = (blockIdx.x * kThreads + threadIdx.x) / kBlockLanes;
+  const uint32_t stride = gridDim.x * (kThreads / kBlockLanes) * kBlocksAhead;
+  for (uint32_t u0 = group / kGroups * kGroups * kBlocksAhead; u0 < p.units; u0 += stride) {
+    uint32_t bits[kBlocksAhead][kWords], row[kBlocksAhead], kb[kBlocksAhead];
+    int cols[kBlocksAhead];
 #pragma unroll
-        for (int i = 0; i < kLaneValues / kV; ++i) {
-          const Pack<T, kV> a = *reinterpret_cast<const Pack<T, kV>*>(src + lane * kLaneValues + i * kV);
+    for (int r = 0; r < kBlocksAhead; ++r) {
+      const uint32_t u = u0 + group % kGroups * kBlocksAhead + r;
+      const bool live = u < p.units;
+      row[r] = live ? quotient(p.blocks, u) : 0;
+      kb[r] = live ? u - row[r] * p.blocks.d : 0;
+      cols[r] = live ? min(p.dim - static_cast<int>(kb[r]) * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
+      const uint32_t t = quotient(p.heads, row[r]);
+      const T* src = x + t * p.x_ts + (row[r] - t * p.heads.d) * p.x_hs + kb[r] * INDEXER_BLOCK;
 #pragma unroll
-          for (int j = 0; j < kV; ++j) v[i * kV + j] = to_float(a.v[j]);
+      for (int i = 0; i < kWords; ++i) bits[r][i] = 0;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          const int c = (q * kBlockLanes + lane) * kPiece;
+          if (c < cols[r]) {
+#pragma unroll
+            for (int i = 0; i < kPieceWords / 4; ++i) {
+              const uint4 a = reinterpret_cast<const uint4*>(src + c)[i];
+              uint32_t* w = &bits[r][q * kPieceWords + 4 * i];
+              w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            }
+          }
+        }
+      } else {
+        T v[kLaneValues];
+#pragma unroll
+        for (int i = 0; i < kLaneValues; ++i) {
+          const int c = lane + i * kBlockLanes;
+          v[i] = c < cols[r] ? src[c] : from_float<T>(0.0f);
+        }
+        memcpy(bits[r], v, sizeof(v));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kBlocksAhead; ++r) {
+      const uint32_t top = max(block_top<T>(bits[r]), kAmaxFloorBits);
+      if (cols[r] == 0) continue;
+      uint8_t* code;
+      float* scale_at;
+      if constexpr (SLOTS) {
+        const int32_t s = p.slots[row[r]];
+        const uint32_t slot = static_cast<uint32_t>(s);
+        if (slot >= p.capacity) {  // negative ones too
+          if (s != -1 && lane == 0 && kb[r] == 0) atomicAdd(&g_guard_hits, 1u);
+          continue;
+        }
+        const uint32_t page = quotient(p.page_size, slot), off = slot - page * p.page_size.d;
+        code = p.codes + page * p.code_ps + off * p.code_ts + kb[r] * INDEXER_BLOCK;
+        scale_at = p.scales + page * p.scale_ps + off * p.scale_ts + kb[r];
+      } else {
+        code = p.codes + row[r] * static_cast<int64_t>(p.dim) + kb[r] * INDEXER_BLOCK;
+        scale_at = p.scales + (row[r] * static_cast<int64_t>(p.blocks.d) + kb[r]);
+      }
+
+      T t[kLaneValues];
+      float v[kLaneValues], scale;
+      memcpy(t, bits[r], sizeof(t));
+#pragma unroll
+      for (int i = 0; i < kLaneValues; ++i) v[i] = to_float(t[i]);
+      uint32_t c[kLaneValues / 4];  // four codes each
+      if (top >= kInfBits) {
+        scale = __uint_as_float(0x7fffffffu);
+#pragma unroll
+        for (int i = 0; i < kLaneValues / 4; ++i) c[i] = 0x7f7f7f7fu;
+      } else if (p.pow2) {
+        // amax = m 2^e, 1 <= m < 2: 448 = 1.75 * 2^8, so 2^(e-8) while m <= 1.75, else 2^(e-7)
+        const uint32_t e = (top >> 23) - 8u + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
+        scale = __uint_as_float(e << 23);
+        const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+        for (int i = 0; i < kLaneValues / 4; ++i) c[i] = codes_of(&v[4 * i], inv) | codes_of(&v[4 * i + 2], inv) << 16;
+      } else {
+        scale = over_448(__uint_as_float(top));
+        // the two quotients enclose the real one by 2^-22 or more on each side
+        const float inv = about_inverse(scale), low = inv * (1.0f - 0x1p-21f), high = inv * (1.0f + 0x1p-21f);
+        uint32_t differ = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneValues / 4; ++i) {
+          c[i] = codes_of(&v[4 * i], low) | codes_of(&v[4 * i + 2], low) << 16;
+          differ |= c[i] ^ (codes_of(&v[4 * i], high) | codes_of(&v[4 * i + 2], high) << 16);
+        }
+        if (differ != 0u) {
+#pragma unroll
+          for (int i = 0; i < kLaneValues / 4; ++i) {
+            c[i] = e4m3x2(quotient_to_odd(v[4 * i], scale, inv), quotient_to_odd(v[4 * i + 1], scale, inv)) |
+                   e4m3x2(quotient_to_odd(v[4 * i + 2], scale, inv), quotient_to_odd(v[4 * i + 3], scale, inv)) << 16;
+          }
+        }
+      }
+      if constexpr (VEC) {
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          const int col = (q * kBlockLanes + lane) * kPiece;
+          if (col < cols[r]) *reinterpret_cast<uint2*>(code + col) = make_uint2(c[2 * q], c[2 * q + 1]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kLaneValues; ++i) v[i] = 0.0f;
+        for (int i = 0; i < kLaneValues; ++i) {
+          const int col = lane + i * kBlockLanes;
+          if (col < cols[r]) code[col] = static_cast<uint8_t>(c[i / 4] >> (8 * (i & 3)));
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLaneValues; ++i) {
-        const int c = lane + i * kBlockLanes;
-        v[i] = c < cols ? to_float(src[c]) : 0.0f;
-      }
-    }
-    uint32_t top = kAmaxFloorBits;
-#pragma unroll
-    for (int i = 0; i < kLaneValues; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-    for (int d = kBlockLanes / 2; d > 0; d /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (!live) continue;
-
-    int64_t slot = row;
-    if (p.slots != nullptr) {
-      slot = p.slots[row];
-      if (slot < 0 || slot >= p.capacity) {
-        if (slot != -1 && lane == 0 && kb == 0) atomicAdd(&g_guard_hits, 1u);
-        continue;
+      if (lane == 0) {
+        if constexpr (SLOTS) *scale_at = scale;
+        else *scale_at = p.weights != nullptr ? p.weights[row[r]] * scale : scale;
       }
     }
-    const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
-    uint8_t* code = p.codes + page * p.code_ps + off * p.code_ts + kb * INDEXER_BLOCK;
-
-    float scale;
-    uint32_t c8[kLaneValues / 2];
-    if (top >= kInfBits) {
-      scale = __uint_as_float(0x7fffffffu);
-#pragma unroll
-      for (int i = 0; i < kLaneValues / 2; ++i) c8[i] = 0x7f7fu;
-    } else if (p.pow2) {
-      // amax = m 2^e, 1 <= m < 2: 448 = 1.75 * 2^8, so 2^(e-8) while m <= 1.75, else 2^(e-7)
-      const uint32_t e = (top >> 23) - 8u + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
-      scale = __uint_as_float(e << 23);
-      const float inv = __uint_as_float((254u - e) << 23);
-#pragma unroll
-      for (int i = 0; i < kLaneValues / 2; ++i) c8[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    } else {
-      scale = __fdiv_rn(__uint_as_float(top), 448.0f);
-      const float inv = __frcp_rn(scale);
-#pragma unroll
-      for (int i = 0; i < kLaneValues / 2; ++i)
-        c8[i] = e4m3x2(quotient_to_odd(v[2 * i], scale, inv), quotient_to_odd(v[2 * i + 1], scale, inv));
-    }
-    if constexpr (VEC) {
-      if (lane * kLaneValues < cols)
-        *reinterpret_cast<uint2*>(code + lane * kLaneValues) =
-            make_uint2(c8[0] | c8[1] << 16, c8[2] | c8[3] << 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLaneValues; ++i) {
-        const int c = lane + i * kBlockLanes;
-        if (c < cols) code[c] = static_cast<uint8_t>(c8[i / 2] >> (8 * (i & 1)));
-      }
-    }
-    if (lane == 0)
-      p.scales[page * p.scale_ps + off * p.scale_ts + kb] =
-          p.weights != nullptr ? p.weights[row] * scale : scale;
   }
 }
 
@@ -159,45 +248,61 @@ struct ReadParams {
   const int32_t* slots;
   void* out;
   int64_t code_ps, code_ts, scale_ps, scale_ts;
-  int64_t units;     // rows * items of a row
-  int64_t capacity;
-  int32_t dim, items, page_size;
+  uint32_t units;     // rows * items of a row
+  uint32_t capacity;
+  Divisor items, page_size;
+  int32_t dim;
 };
 
-// VEC: an item is 8 columns (8 bytes in, 16 or 32 out); otherwise one column.
-template <typename T, bool VEC>
+// An item is V columns of a row: V * sizeof(T) = 32 bytes of output in one store, or one column (V = 1).
+template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-  constexpr int kV = VEC ? 8 : 1;
   begin_after_prior_grids();
   T* out = static_cast<T*>(p.out);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u < p.units;
-       u += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t row = u / p.items;
-    const int item = static_cast<int>(u - row * p.items);
-    const int col = item * kV;
-    const int64_t slot = p.slots[row];
-    const bool inside = slot >= 0 && slot < p.capacity;
-    if (!inside && slot != -1 && item == 0) atomicAdd(&g_guard_hits, 1u);
-    float f = 0.0f;
-    Pack<uint8_t, kV> c = {};
-    if (inside) {
-      const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
-      c = *reinterpret_cast<const Pack<uint8_t, kV>*>(p.codes + page * p.code_ps + off * p.code_ts + col);
-      f = p.scales[page * p.scale_ps + off * p.scale_ts + col / INDEXER_BLOCK];
+  const uint32_t threads = gridDim.x * kThreads;
+  for (uint32_t u0 = blockIdx.x * kThreads + threadIdx.x; u0 < p.units; u0 += threads * kRounds) {
+    uint32_t row[kRounds], col[kRounds];
+    int32_t slot[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t u = u0 + r * threads;
+      row[r] = u < p.units ? quotient(p.items, u) : 0;
+      col[r] = u < p.units ? (u - row[r] * p.items.d) * V : 0;
+      slot[r] = u < p.units ? p.slots[row[r]] : -1;
     }
-    T y[kV];
+    Pack<uint8_t, V> c[kRounds];
+    float f[kRounds];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const __half_raw h = __nv_cvt_fp8_to_halfraw(c.v[i], __NV_E4M3);
-      y[i] = from_float<T>(__half2float(__half(h)) * f);
+    for (int r = 0; r < kRounds; ++r) {
+      f[r] = 0.0f;
+      c[r] = {};
+      if (static_cast<uint32_t>(slot[r]) < p.capacity) {
+        const uint32_t page = quotient(p.page_size, slot[r]), off = slot[r] - page * p.page_size.d;
+        c[r] = *reinterpret_cast<const Pack<uint8_t, V>*>(p.codes + page * p.code_ps + off * p.code_ts + col[r]);
+        f[r] = p.scales[page * p.scale_ps + off * p.scale_ts + col[r] / INDEXER_BLOCK];
+      } else if (slot[r] != -1 && col[r] == 0) {
+        atomicAdd(&g_guard_hits, 1u);
+      }
     }
-    constexpr int kS = kV * sizeof(T) < 16 ? kV : 16 / sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kV / kS; ++i) {
-      Pack<T, kS> o;
+    for (int r = 0; r < kRounds; ++r) {
+      if (u0 + r * threads >= p.units) break;
+      T* dst = out + static_cast<int64_t>(row[r]) * p.dim + col[r];
+      if constexpr (V == 1) {
+        *dst = from_float<T>(__half2float(__half(__nv_cvt_fp8_to_halfraw(c[r].v[0], __NV_E4M3))) * f[r]);
+      } else {
+        T y[V];
 #pragma unroll
-      for (int j = 0; j < kS; ++j) o.v[j] = y[i * kS + j];
-      *reinterpret_cast<Pack<T, kS>*>(out + row * p.dim + col + i * kS) = o;
+        for (int i = 0; i < V / 2; ++i) {
+          const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(c[r].v[2 * i] | c[r].v[2 * i + 1] << 8);
+          const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+          y[2 * i] = from_float<T>(v.x * f[r]);
+          y[2 * i + 1] = from_float<T>(v.y * f[r]);
+        }
+        uint32_t words[8];
+        memcpy(words, y, sizeof(words));
+        store32(dst, words);
+      }
     }
   }
 }
@@ -209,38 +314,63 @@ unsigned grid_for(int64_t threads, int sms) {
 
 template <typename T>
 cudaError_t launch_quantise(const QuantParams& p, bool vec, int sms, cudaStream_t stream) {
-  const unsigned grid = grid_for((p.units + 1) / 2 * 2 * kBlockLanes, sms);
-  return vec ? launch(quantise_kernel<T, true>, grid, kThreads, 0, stream, p)
-             : launch(quantise_kernel<T, false>, grid, kThreads, 0, stream, p);
+  constexpr int64_t kWarpUnits = 32 / kBlockLanes * kBlocksAhead;
+  const unsigned grid = grid_for((static_cast<int64_t>(p.units) + kWarpUnits - 1) / kWarpUnits * 32, sms);
+  if (p.slots != nullptr)
+    return vec ? launch(quantise_kernel<T, true, true>, grid, kThreads, 0, stream, p)
+               : launch(quantise_kernel<T, false, true>, grid, kThreads, 0, stream, p);
+  return vec ? launch(quantise_kernel<T, true, false>, grid, kThreads, 0, stream, p)
+             : launch(quantise_kernel<T, false, false>, grid, kThreads, 0, stream, p);
 }
 
-int run_quantise(QuantParams p, int32_t dtype, int64_t rows, cudaStream_t stream) {
+// The kernels number rows' parts in 31 bits: longer calls are cut into launches of so many rows.
+int64_t rows_of_launch(int64_t parts_of_row) { return (INT64_C(1) << 30) / parts_of_row; }
+
+// heads: rows of a token (one slot, or `heads` rows in a row of the outputs).
+int run_quantise(QuantParams p, int32_t dtype, int64_t tokens, int64_t heads, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return status_of(e);
-  p.blocks = (p.dim + INDEXER_BLOCK - 1) / INDEXER_BLOCK;
-  p.units = rows * p.blocks;
+  const int64_t blocks = (p.dim + INDEXER_BLOCK - 1) / INDEXER_BLOCK;
+  p.blocks = divisor(blocks);
   // rows a constant step apart need no division
-  if (p.heads > 1 && p.x_ts == p.heads * p.x_hs) {
+  if (heads > 1 && p.x_ts == heads * p.x_hs && tokens * heads <= INT32_MAX) {
+    tokens *= heads;
     p.x_ts = p.x_hs;
-    p.heads = 1;
+    heads = 1;
   }
   const int64_t values = static_cast<int64_t>(16 / dtype_bytes(dtype));
-  const bool vec = p.dim % kLaneValues == 0 && p.x_ts % values == 0 && p.x_hs % values == 0 &&
+  const bool vec = p.dim % kPiece == 0 && p.x_ts % values == 0 && p.x_hs % values == 0 &&
                    (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 &&
                    p.code_ts % 8 == 0 && p.code_ps % 8 == 0 &&
                    (reinterpret_cast<uintptr_t>(p.codes) & 7u) == 0;
-  if (dtype == INDEXER_BF16) e = launch_quantise<__nv_bfloat16>(p, vec, sms, stream);
-  else if (dtype == INDEXER_FP16) e = launch_quantise<__half>(p, vec, sms, stream);
-  else e = launch_quantise<float>(p, vec, sms, stream);
-  return status_of(e);
+  if (heads > rows_of_launch(blocks)) return TOPK_ERR_INVALID_ARGUMENT;
+  p.heads = divisor(heads);
+  const int64_t step = rows_of_launch(blocks * heads);
+  for (int64_t t = 0; t < tokens; t += step) {
+    const int64_t n = tokens - t < step ? tokens - t : step;
+    p.units = static_cast<uint32_t>(n * heads * blocks);
+    if (dtype == INDEXER_BF16) e = launch_quantise<__nv_bfloat16>(p, vec, sms, stream);
+    else if (dtype == INDEXER_FP16) e = launch_quantise<__half>(p, vec, sms, stream);
+    else e = launch_quantise<float>(p, vec, sms, stream);
+    if (e != cudaSuccess) return status_of(e);
+    p.x = static_cast<const char*>(p.x) + n * p.x_ts * static_cast<int64_t>(dtype_bytes(dtype));
+    if (p.slots != nullptr) {
+      p.slots += n;
+    } else {
+      p.codes += n * heads * p.code_ts;
+      p.scales += n * heads * p.scale_ts;
+    }
+    if (p.weights != nullptr) p.weights += n * heads;
+  }
+  return TOPK_OK;
 }
 
 template <typename T>
 cudaError_t launch_read(const ReadParams& p, bool vec, int sms, cudaStream_t stream) {
-  const unsigned grid = grid_for(p.units, sms);
-  return vec ? launch(read_kernel<T, true>, grid, kThreads, 0, stream, p)
-             : launch(read_kernel<T, false>, grid, kThreads, 0, stream, p);
+  const unsigned grid = grid_for((static_cast<int64_t>(p.units) + kRounds - 1) / kRounds, sms);
+  return vec ? launch(read_kernel<T, 32 / sizeof(T)>, grid, kThreads, 0, stream, p)
+             : launch(read_kernel<T, 1>, grid, kThreads, 0, stream, p);
 }
 
 bool dtype_ok(int32_t dtype) { return dtype >= INDEXER_BF16 && dtype <= INDEXER_FP32; }
@@ -284,13 +414,11 @@ int indexer_quantise(const void* x, int64_t x_token_stride, int64_t x_head_strid
   p.weights = weights;
   p.x_ts = tokens > 1 ? x_token_stride : 0;
   p.x_hs = heads > 1 ? x_head_stride : 0;
-  p.heads = heads;
   p.dim = dim;
   p.pow2 = scale_format == INDEXER_SCALE_POW2;
-  p.page_size = 1;  // row r is page r: its own place in contiguous outputs
-  p.code_ps = dim;
-  p.scale_ps = (dim + INDEXER_BLOCK - 1) / INDEXER_BLOCK;
-  return run_quantise(p, dtype, tokens * heads, stream);
+  p.code_ts = dim;  // contiguous outputs
+  p.scale_ts = (dim + INDEXER_BLOCK - 1) / INDEXER_BLOCK;
+  return run_quantise(p, dtype, tokens, heads, stream);
 }
 
 int indexer_cache_write(const void* x, int64_t x_token_stride, int32_t dtype, int64_t tokens,
@@ -310,16 +438,15 @@ int indexer_cache_write(const void* x, int64_t x_token_stride, int32_t dtype, in
   p.scales = cache->scales;
   p.slots = slots;
   p.x_ts = tokens > 1 ? x_token_stride : 0;
-  p.heads = 1;
   p.dim = cache->dim;
   p.pow2 = scale_format == INDEXER_SCALE_POW2;
-  p.page_size = cache->page_size;
+  p.page_size = divisor(cache->page_size);
   p.code_ps = cache->num_pages > 1 ? cache->code_page_stride : 0;
   p.code_ts = cache->page_size > 1 ? cache->code_token_stride : 0;
   p.scale_ps = cache->scale_page_stride;
   p.scale_ts = cache->scale_token_stride;
-  p.capacity = cache->num_pages * cache->page_size;
-  return run_quantise(p, dtype, tokens, stream);
+  p.capacity = static_cast<uint32_t>(cache->num_pages * cache->page_size);
+  return run_quantise(p, dtype, tokens, 1, stream);
 }
 
 int indexer_cache_read(const indexer_cache_t* cache, const int32_t* slots, int64_t rows,
@@ -339,20 +466,29 @@ int indexer_cache_read(const indexer_cache_t* cache, const int32_t* slots, int64
   p.slots = slots;
   p.out = out;
   p.dim = cache->dim;
-  p.page_size = cache->page_size;
+  p.page_size = divisor(cache->page_size);
   p.code_ps = cache->num_pages > 1 ? cache->code_page_stride : 0;
   p.code_ts = cache->page_size > 1 ? cache->code_token_stride : 0;
   p.scale_ps = cache->scale_page_stride;
   p.scale_ts = cache->scale_token_stride;
-  p.capacity = cache->num_pages * cache->page_size;
-  const bool vec = p.dim % 8 == 0 && p.code_ts % 8 == 0 && p.code_ps % 8 == 0 && aligned(p.codes, 8) &&
-                   aligned(out, 16);
-  p.items = vec ? p.dim / 8 : p.dim;
-  p.units = rows * p.items;
-  if (dtype == INDEXER_BF16) e = launch_read<__nv_bfloat16>(p, vec, sms, stream);
-  else if (dtype == INDEXER_FP16) e = launch_read<__half>(p, vec, sms, stream);
-  else e = launch_read<float>(p, vec, sms, stream);
-  return status_of(e);
+  p.capacity = static_cast<uint32_t>(cache->num_pages * cache->page_size);
+  const int32_t columns = 32 / static_cast<int32_t>(dtype_bytes(dtype));  // of a 32-byte store
+  const bool vec = p.dim % columns == 0 && p.code_ts % columns == 0 && p.code_ps % columns == 0 &&
+                   aligned(p.codes, columns) && aligned(out, 32);
+  const int32_t items = vec ? p.dim / columns : p.dim;
+  p.items = divisor(items);
+  const int64_t step = rows_of_launch(items);
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t n = rows - r < step ? rows - r : step;
+    p.units = static_cast<uint32_t>(n * items);
+    if (dtype == INDEXER_BF16) e = launch_read<__nv_bfloat16>(p, vec, sms, stream);
+    else if (dtype == INDEXER_FP16) e = launch_read<__half>(p, vec, sms, stream);
+    else e = launch_read<float>(p, vec, sms, stream);
+    if (e != cudaSuccess) return status_of(e);
+    p.slots += n;
+    p.out = static_cast<char*>(p.out) + n * p.dim * static_cast<int64_t>(dtype_bytes(dtype));
+  }
+  return TOPK_OK;
 }
 
 int indexer_guard_hits(uint64_t* hits) {

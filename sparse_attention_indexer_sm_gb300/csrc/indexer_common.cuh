@@ -37,6 +37,18 @@ inline bool cache_ok(const indexer_cache_t* c) {
          (!pages || (c->code_page_stride >= c->dim && c->scale_page_stride >= nb));
 }
 
+// Division of numbers below 2^31 by a constant of the launch: n / d = (n * magic) >> (31 + shift).
+struct Divisor {
+  uint32_t d, magic, shift;
+};
+
+inline Divisor divisor(int64_t d) {
+  Divisor r = {static_cast<uint32_t>(d), 0, 0};
+  while ((int64_t(1) << r.shift) < d) ++r.shift;
+  r.magic = static_cast<uint32_t>(((uint64_t(1) << (31 + r.shift)) + d - 1) / d);
+  return r;
+}
+
 inline size_t dtype_bytes(int32_t dtype) { return dtype == INDEXER_FP32 ? 4u : 2u; }
 
 // The SM count of the current device, asked once for each device.
@@ -76,6 +88,10 @@ inline int status_of(cudaError_t e) {
 
 #ifdef __CUDACC__
 
+__device__ __forceinline__ uint32_t quotient(const Divisor& d, uint32_t n) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * d.magic) >> 31 >> d.shift);
+}
+
 // Programmatic dependent launch: the next kernel of the stream may be scheduled from
 // here on, and nothing of the previous one is read or overwritten before it has ended.
 __device__ __forceinline__ void begin_after_prior_grids() {
@@ -97,6 +113,13 @@ template <> __device__ __forceinline__ __half from_float<__half>(float v) { retu
 template <typename T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
   T v[N];
 };
+
+// 32 bytes in one access, on a boundary of 32.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 
 #endif  // __CUDACC__
 

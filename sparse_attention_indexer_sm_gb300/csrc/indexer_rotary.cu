@@ -1,14 +1,15 @@
 // Rotary positions: pairs of columns turned by an angle of their own, position * frequency.
 //
-// Bound by memory: every element is read once and written once, about 10 operations each.
+// Bound by memory: every element is read once and written once, with a few operations each.
 // - The angle. position * frequency in radians loses the fraction of a turn for far
 //   positions in fp32 (2^20 positions leave 4 bits of it), and GB300 has almost no fp64
-//   rate. A frequency is therefore turned into a 64-bit fixed-point fraction of a turn,
-//   once for each CTA (the only fp64 operations); position * fraction wraps modulo one turn
-//   by itself, in integers and without any rounding, and its top 32 bits are the angle.
-// - The split. A thread keeps the angles of one token's few pairs in registers and walks
-//   over a group of heads with them, so that sine and cosine are computed once for the
-//   group. Lanes cover a row's columns, so accesses are coalesced.
+//   rate. A frequency's bits are therefore turned into a 64-bit fixed-point fraction of a turn by
+//   one integer product; position * fraction wraps modulo one turn by itself, without any
+//   rounding, and its top 32 bits are the angle.
+// - The split. A CTA owns a tile of tokens and heads. Its threads first leave the tile's sines and cosines
+//   in shared memory, each computed once, then walk over the rows in 16-byte pieces, four pieces in
+//   flight in each thread. Sines kept in registers over a thread's heads took up to 232
+//   registers and left the loads' latency bare (8192 x 64 x 128 in bf16, half of each row turned: 89 us).
 
 #include "indexer_common.cuh"
 
@@ -16,7 +17,8 @@ namespace indexer_gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairsShared = 1024;  // pairs whose steps fit the shared array
+constexpr int kAhead = 4;          // pieces whose loads are in flight
+constexpr int kMaxAngles = 2048;   // sines of a tile
 
 struct RotaryParams {
   const void* x;
@@ -24,124 +26,198 @@ struct RotaryParams {
   const int32_t* positions;
   const double* freqs;
   int64_t x_ts, x_hs, out_ts, out_hs;
-  int64_t units;     // tokens * head groups * items
-  int32_t heads, dim, pairs, start;
-  int32_t group, groups;  // heads of a group, groups
-  int32_t items, rot_items;  // threads' shares of a row; the first rot_items of them rotate
+  Divisor pairs, turn_items, copy_items;  // pairs of a segment; a row's pieces that turn, and that are copied
+  Divisor tile_heads, head_tiles, segments;
+  int32_t tokens, heads, all_pairs, start, tile_tokens;
   float scale, sign;
 };
 
-// One position step as a fraction of a turn, in 2^-64 turns.
+// One position step as a fraction of a turn, in 2^-64 turns: the frequency's 53 bits times 2^66 / (2 pi).
 __device__ __forceinline__ uint64_t turn_step(double freq) {
-  double t = freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return static_cast<uint64_t>(t * 18446744073709551616.0);
+  constexpr uint64_t kPerTurn = 0xa2f9836e4e441529ull;  // floor(2^66 / (2 pi))
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(freq));
+  const int field = static_cast<int>(bits >> 52) & 0x7ff;
+  const uint64_t m = (bits & 0xfffffffffffffull) | (field != 0 ? 1ull << 52 : 0ull);
+  const uint64_t high = __umul64hi(m, kPerTurn), low = m * kPerTurn;
+  const int shift = 54 + 1023 - (field != 0 ? field : 1);  // to the right
+  uint64_t r;
+  if (shift >= 128) r = 0;
+  else if (shift >= 64) r = high >> (shift - 64);
+  else if (shift > 0) r = high << (64 - shift) | low >> shift;
+  else r = shift > -64 ? low << -shift : 0;
+  return bits >> 63 ? 0 - r : r;
 }
 
-// V: values of one access. kHalf: the layout. A rotating item is V pairs (half layout, two
+// V: values of one access. kHalf: the layout. A piece that turns is V pairs (half layout, two
 // accesses) or V / 2 pairs (interleaved, one access; one pair and two accesses at V = 1).
 template <typename T, int V, bool kHalf>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
-  constexpr int kPairs = kHalf || V == 1 ? V : V / 2;
-  __shared__ uint64_t steps[kMaxPairsShared];
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams p) {
+  constexpr bool kTwo = kHalf || V == 1;
+  constexpr int kPairs = kTwo ? V : V / 2;
+  __shared__ __align__(16) float cosines[kMaxAngles], sines[kMaxAngles];
   begin_after_prior_grids();
-  const bool shared_steps = p.pairs <= kMaxPairsShared;
-  if (shared_steps) {
-    for (int i = threadIdx.x; i < p.pairs; i += kThreads) steps[i] = turn_step(p.freqs[i]);
-    __syncthreads();
-  }
-  using P = Pack<T, V>;
-  const T* x = static_cast<const T*>(p.x);
-  T* out = static_cast<T*>(p.out);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u < p.units;
-       u += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t row = u / p.items;
-    const int item = static_cast<int>(u - row * p.items);
-    const int64_t t = row / p.groups;
-    const int h0 = static_cast<int>(row - t * p.groups) * p.group;
-    const int h1 = min(h0 + p.group, p.heads);
-    const T* src = x + t * p.x_ts + static_cast<int64_t>(h0) * p.x_hs;
-    T* dst = out + t * p.out_ts + static_cast<int64_t>(h0) * p.out_hs;
-    if (item >= p.rot_items) {
-      int col = (item - p.rot_items) * V;
-      if (col >= p.start) col += 2 * p.pairs;
-      for (int h = h0; h < h1; ++h, src += p.x_hs, dst += p.out_hs)
-        *reinterpret_cast<P*>(dst + col) = *reinterpret_cast<const P*>(src + col);
-      continue;
-    }
-    const int first = item * kPairs;
-    const int64_t pos = p.positions[t];
-    float c[kPairs], s[kPairs];
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const uint64_t step = shared_steps ? steps[first + i] : turn_step(p.freqs[first + i]);
-      const uint64_t phase = static_cast<uint64_t>(pos) * step;
+  // this CTA's segment of pairs, tile of heads and tile of tokens
+  const uint32_t block = quotient(p.segments, blockIdx.x), segment = blockIdx.x - block * p.segments.d;
+  const uint32_t tile = quotient(p.head_tiles, block);
+  const int h0 = static_cast<int>((block - tile * p.head_tiles.d) * p.tile_heads.d);
+  const int t0 = static_cast<int>(tile) * p.tile_tokens;
+  const uint32_t heads = min(static_cast<int>(p.tile_heads.d), p.heads - h0);
+  const uint32_t tokens = min(p.tile_tokens, p.tokens - t0);
+  const uint32_t first_pair = segment * p.pairs.d, pairs = min(p.pairs.d, p.all_pairs - first_pair);
+
+  for (uint32_t i = threadIdx.x; i < tokens * p.pairs.d; i += kThreads) {
+    const uint32_t t = quotient(p.pairs, i), k = i - t * p.pairs.d;
+    if (k < pairs) {
+      const int64_t pos = p.positions[t0 + t];
+      const uint64_t phase = static_cast<uint64_t>(pos) * turn_step(p.freqs[first_pair + k]);
       // top 32 bits, signed: half turns in [-1, 1)
       const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      sincospif(half_turns, &s[i], &c[i]);
-      c[i] *= p.scale;
-      s[i] *= p.scale * p.sign;
+      float s, c;
+      sincospif(half_turns, &s, &c);
+      cosines[i] = c * p.scale;
+      sines[i] = s * p.scale * p.sign;
     }
-    if constexpr (kHalf || V == 1) {
-      const int ca = p.start + (kHalf ? first : 2 * first);
-      const int cb = ca + (kHalf ? p.pairs : 1);
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h, src += p.x_hs, dst += p.out_hs) {
-        const P a = *reinterpret_cast<const P*>(src + ca);
-        const P b = *reinterpret_cast<const P*>(src + cb);
-        P ya, yb;
+  }
+  __syncthreads();
+
+  using P = Pack<T, V>;
+  const T* const x = static_cast<const T*>(p.x) + t0 * p.x_ts + h0 * p.x_hs;
+  T* const out = static_cast<T*>(p.out) + t0 * p.out_ts + h0 * p.out_hs;
+  const uint32_t rows = tokens * heads;
+  // Row r of the tile is head r / tokens of token r % tokens where tokens lie closer, and the other way round;
+  // here heads are the inner axis: neighbouring pieces of a token's heads.
+  auto place = [&](uint32_t r, uint32_t* t) {
+    *t = heads == p.tile_heads.d ? quotient(p.tile_heads, r) : r / heads;
+    return r - *t * heads;
+  };
+
+  const uint32_t turning = rows * p.turn_items.d;
+  for (uint32_t u0 = threadIdx.x; u0 < turning; u0 += kThreads * kAhead) {
+    P a[kAhead], b[kAhead];
+    uint32_t angle[kAhead];
+    T* dst[kAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float fa = to_float(a.v[i]), fb = to_float(b.v[i]);
-          ya.v[i] = from_float<T>(fmaf(fa, c[i], -fb * s[i]));
-          yb.v[i] = from_float<T>(fmaf(fa, s[i], fb * c[i]));
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t u = u0 + k * kThreads;
+      dst[k] = nullptr;
+      if (u < turning) {
+        const uint32_t r = quotient(p.turn_items, u), first = (u - r * p.turn_items.d) * kPairs;
+        if (first < pairs) {
+          uint32_t t;
+          const uint32_t h = place(r, &t);
+          angle[k] = t * p.pairs.d + first;
+          const uint32_t col = p.start + (kHalf ? 1 : 2) * (first_pair + first);
+          const T* src = x + t * p.x_ts + h * p.x_hs + col;
+          dst[k] = out + t * p.out_ts + h * p.out_hs + col;
+          a[k] = *reinterpret_cast<const P*>(src);
+          if constexpr (kTwo) b[k] = *reinterpret_cast<const P*>(src + (kHalf ? p.all_pairs : 1));
         }
-        *reinterpret_cast<P*>(dst + ca) = ya;
-        *reinterpret_cast<P*>(dst + cb) = yb;
-      }
-    } else {
-      const int col = p.start + 2 * first;
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h, src += p.x_hs, dst += p.out_hs) {
-        const P a = *reinterpret_cast<const P*>(src + col);
-        P y;
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const float fa = to_float(a.v[2 * i]), fb = to_float(a.v[2 * i + 1]);
-          y.v[2 * i] = from_float<T>(fmaf(fa, c[i], -fb * s[i]));
-          y.v[2 * i + 1] = from_float<T>(fmaf(fa, s[i], fb * c[i]));
-        }
-        *reinterpret_cast<P*>(dst + col) = y;
       }
     }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (dst[k] == nullptr) continue;
+      float c[kPairs], s[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; i += kPairs % 4 == 0 ? 4 : 1) {
+        if constexpr (kPairs % 4 == 0) {
+          const float4 fc = *reinterpret_cast<const float4*>(&cosines[angle[k] + i]);
+          const float4 fs = *reinterpret_cast<const float4*>(&sines[angle[k] + i]);
+          c[i] = fc.x, c[i + 1] = fc.y, c[i + 2] = fc.z, c[i + 3] = fc.w;
+          s[i] = fs.x, s[i + 1] = fs.y, s[i + 2] = fs.z, s[i + 3] = fs.w;
+        } else {
+          c[i] = cosines[angle[k] + i];
+          s[i] = sines[angle[k] + i];
+        }
+      }
+      P ya, yb;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float fa = to_float(kTwo ? a[k].v[i] : a[k].v[2 * i]);
+        const float fb = to_float(kTwo ? b[k].v[i] : a[k].v[2 * i + 1]);
+        (kTwo ? ya.v[i] : ya.v[2 * i]) = from_float<T>(fmaf(fa, c[i], -fb * s[i]));
+        (kTwo ? yb.v[i] : ya.v[2 * i + 1]) = from_float<T>(fmaf(fa, s[i], fb * c[i]));
+      }
+      *reinterpret_cast<P*>(dst[k]) = ya;
+      if constexpr (kTwo) *reinterpret_cast<P*>(dst[k] + (kHalf ? p.all_pairs : 1)) = yb;
+    }
+  }
+
+  if (segment != 0) return;
+  const uint32_t copying = p.copy_items.d == 0 ? 0 : rows * p.copy_items.d;
+  for (uint32_t u0 = threadIdx.x; u0 < copying; u0 += kThreads * kAhead) {
+    P a[kAhead];
+    T* dst[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t u = u0 + k * kThreads;
+      dst[k] = nullptr;
+      if (u < copying) {
+        const uint32_t r = quotient(p.copy_items, u);
+        int col = static_cast<int>(u - r * p.copy_items.d) * V;
+        if (col >= p.start) col += 2 * p.all_pairs;
+        uint32_t t;
+        const uint32_t h = place(r, &t);
+        a[k] = *reinterpret_cast<const P*>(x + t * p.x_ts + h * p.x_hs + col);
+        dst[k] = out + t * p.out_ts + h * p.out_hs + col;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (dst[k] != nullptr) *reinterpret_cast<P*>(dst[k]) = a[k];
   }
 }
 
 template <typename T>
-cudaError_t launch_rotary(RotaryParams p, int64_t tokens, bool half, bool in_place, int sms,
+cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half, bool in_place, int sms,
                           cudaStream_t stream) {
   // 16-byte accesses where every row, and the pairs' two halves, start on 16 bytes
   constexpr int kV = 16 / sizeof(T);
-  const int64_t all = p.x_ts | p.x_hs | p.out_ts | p.out_hs | p.dim | p.start | (half ? p.pairs : 2 * p.pairs);
+  const int64_t all = p.x_ts | p.x_hs | p.out_ts | p.out_hs | dim | p.start | (half ? p.all_pairs : 2 * p.all_pairs);
   const bool wide = all % kV == 0 &&
                     ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15u) == 0;
   const int v = wide ? kV : 1;
   const int pairs_of_item = half || v == 1 ? v : v / 2;
-  p.rot_items = p.pairs / pairs_of_item;
-  p.items = p.rot_items + (in_place ? 0 : (p.dim - 2 * p.pairs) / v);
-  // Heads of a group: eight share a sine, fewer where that leaves threads of the chip idle.
-  p.group = 8;
-  while (p.group > 1 && tokens * ((p.heads + p.group - 1) / p.group) * p.items < int64_t(sms) * 2048) p.group /= 2;
-  p.groups = (p.heads + p.group - 1) / p.group;
-  p.units = tokens * p.groups * p.items;
-  const int64_t blocks = (p.units + kThreads - 1) / kThreads;
-  const unsigned grid = static_cast<unsigned>(blocks < int64_t(sms) * 8 ? blocks : int64_t(sms) * 8);
-  if (wide) {
-    return half ? launch(rotary_kernel<T, kV, true>, grid, kThreads, 0, stream, p)
-                : launch(rotary_kernel<T, kV, false>, grid, kThreads, 0, stream, p);
+  const int64_t segments = (p.all_pairs + kMaxAngles - 1) / kMaxAngles;
+  const int64_t pairs = segments > 1 ? kMaxAngles : p.all_pairs;
+  const int64_t turn_items = pairs / pairs_of_item, copy_items = in_place ? 0 : (dim - 2 * p.all_pairs) / v;
+  // Pieces of a CTA: eight for each thread where the chip has enough of them to do, one otherwise. All heads of one
+  // or more tokens, or a part of one token's heads.
+  const int64_t row = turn_items + copy_items, total = tokens * p.heads * row;
+  const int64_t pieces = total >= int64_t(sms) * 2048 ? 8 * kThreads : total >= int64_t(sms) * 1024 ? 4 * kThreads : kThreads;
+  int64_t heads = pieces / row < 1 ? 1 : pieces / row < p.heads ? pieces / row : p.heads;
+  const int64_t head_tiles = (p.heads + heads - 1) / heads;
+  heads = (p.heads + head_tiles - 1) / head_tiles;
+  int64_t tile_tokens = heads == p.heads ? pieces / (row * heads) : 1;
+  if (tile_tokens > kMaxAngles / pairs) tile_tokens = kMaxAngles / pairs;
+  if (tile_tokens < 1) tile_tokens = 1;
+  p.tile_tokens = static_cast<int32_t>(tile_tokens);
+  p.tile_heads = divisor(heads);
+  p.head_tiles = divisor(head_tiles);
+  p.segments = divisor(segments);
+  p.pairs = divisor(pairs);
+  p.turn_items = divisor(turn_items);
+  p.copy_items = copy_items > 0 ? divisor(copy_items) : Divisor{0, 0, 0};
+  // a launch has fewer than 2^31 CTAs: a longer call is cut into launches of so many tokens
+  if (head_tiles * segments > INT64_C(1) << 30) return cudaErrorInvalidValue;
+  const int64_t step = (INT64_C(1) << 30) / (head_tiles * segments) * tile_tokens;
+  for (int64_t t = 0; t < tokens; t += step) {
+    const int64_t n = tokens - t < step ? tokens - t : step;
+    p.tokens = static_cast<int32_t>(n);
+    const unsigned grid = static_cast<unsigned>((n + tile_tokens - 1) / tile_tokens * head_tiles * segments);
+    cudaError_t e;
+    if (wide)
+      e = half ? launch(rotary_kernel<T, kV, true>, grid, kThreads, 0, stream, p)
+               : launch(rotary_kernel<T, kV, false>, grid, kThreads, 0, stream, p);
+    else
+      e = half ? launch(rotary_kernel<T, 1, true>, grid, kThreads, 0, stream, p)
+               : launch(rotary_kernel<T, 1, false>, grid, kThreads, 0, stream, p);
+    if (e != cudaSuccess) return e;
+    p.x = static_cast<const T*>(p.x) + n * p.x_ts;
+    p.out = static_cast<T*>(p.out) + n * p.out_ts;
+    p.positions += n;
   }
-  return half ? launch(rotary_kernel<T, 1, true>, grid, kThreads, 0, stream, p)
-              : launch(rotary_kernel<T, 1, false>, grid, kThreads, 0, stream, p);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -173,7 +249,8 @@ extern "C" int indexer_rotary(const void* x, int64_t x_token_stride, int64_t x_h
   if (inner < dim || (outer != INT64_MAX && (outer - dim) / inner < inner_n - 1))
     return TOPK_ERR_INVALID_ARGUMENT;
   const uintptr_t low = static_cast<uintptr_t>(dtype_bytes(dtype)) - 1;
-  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & low) != 0)
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & low) != 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0)
     return TOPK_ERR_INVALID_ARGUMENT;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
@@ -189,15 +266,14 @@ extern "C" int indexer_rotary(const void* x, int64_t x_token_stride, int64_t x_h
   p.out_ts = tokens > 1 ? out_token_stride : 0;
   p.out_hs = heads > 1 ? out_head_stride : 0;
   p.heads = heads;
-  p.dim = dim;
-  p.pairs = rot_dim / 2;
+  p.all_pairs = rot_dim / 2;
   p.start = start;
   p.scale = scale;
   p.sign = transpose != 0 ? -1.0f : 1.0f;
   const bool half = layout == INDEXER_LAYOUT_HALF;
   const bool in_place = x == out && p.x_ts == p.out_ts && p.x_hs == p.out_hs;
-  if (dtype == INDEXER_BF16) e = launch_rotary<__nv_bfloat16>(p, tokens, half, in_place, sms, stream);
-  else if (dtype == INDEXER_FP16) e = launch_rotary<__half>(p, tokens, half, in_place, sms, stream);
-  else e = launch_rotary<float>(p, tokens, half, in_place, sms, stream);
+  if (dtype == INDEXER_BF16) e = launch_rotary<__nv_bfloat16>(p, tokens, dim, half, in_place, sms, stream);
+  else if (dtype == INDEXER_FP16) e = launch_rotary<__half>(p, tokens, dim, half, in_place, sms, stream);
+  else e = launch_rotary<float>(p, tokens, dim, half, in_place, sms, stream);
   return status_of(e);
 }

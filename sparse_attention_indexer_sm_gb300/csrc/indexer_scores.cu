@@ -73,7 +73,7 @@ struct ScoresParams {
   int64_t num_pages, scale_ps, scale_ts, pt_stride;
   int64_t row_len, items, slices;  // slices: items of one chunk of tiles (sequences * groups)
   int32_t page_size, piece_rows;
-  uint32_t page_magic, page_shift; // row / page_size = (row * magic) >> (31 + shift) for rows below 2^31
+  Divisor page_div;                // by page_size
   int32_t quads;                   // pages hold whole quads of keys: 1; and their scales are aligned 16-byte quads: 2
   int32_t queries, heads, group, groups;
   int32_t tiles, chunk;            // tiles of a row; tiles of an item
@@ -265,9 +265,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t page_of(const ScoresParams& p, uint32_t row) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(row) * p.page_magic) >> 31 >> p.page_shift);
-}
+__device__ __forceinline__ uint32_t page_of(const ScoresParams& p, uint32_t row) { return quotient(p.page_div, row); }
 
 // One item: `count` queries from `query` on (rows of seq_lens and out, all of sequence b)
 // against tiles [first, end); tiles from `seen` on have no key that any of the queries sees.
@@ -826,8 +824,7 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   p.page_size = cache->page_size;
   p.piece_rows = cache->page_size & -cache->page_size;
   if (p.piece_rows > kTile) p.piece_rows = kTile;
-  while ((int64_t(1) << p.page_shift) < p.page_size) ++p.page_shift;
-  p.page_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + p.page_shift)) + p.page_size - 1) / p.page_size);
+  p.page_div = divisor(p.page_size);
   p.quads = p.page_size % 4 != 0 ? 0
             : p.scale_ts == 1 && p.scale_ps % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0 ? 2 : 1;
   p.queries = queries;
