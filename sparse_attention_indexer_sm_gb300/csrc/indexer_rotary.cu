@@ -7,8 +7,9 @@
 //   one integer product; position * fraction wraps modulo one turn by itself, without any
 //   rounding, and its top 32 bits are the angle.
 // - The split. A CTA owns a tile of tokens and heads. Its threads first leave the tile's sines and cosines
-//   in shared memory, each computed once, then walk over the rows in 16-byte pieces, four pieces in
-//   flight in each thread. Sines kept in registers over a thread's heads took up to 232
+//   in shared memory, each computed once, then walk over the rows in 16-byte pieces. Many small CTAs
+//   hide the loads' latency better than several pieces in flight in each thread (one piece and six CTAs an SM
+//   against two and five: 8192 x 64 x 128 in bf16, half of each row turned, 48 against 52 us). Sines kept in registers over a thread's heads took up to 232
 //   registers and left the loads' latency bare (8192 x 64 x 128 in bf16, half of each row turned: 89 us).
 
 #include "indexer_common.cuh"
@@ -17,7 +18,7 @@ namespace indexer_gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;          // pieces whose loads are in flight
+constexpr int kResident = 6;       // CTAs of an SM
 constexpr int kMaxAngles = 2048;   // sines of a tile
 
 struct RotaryParams {
@@ -48,10 +49,31 @@ __device__ __forceinline__ uint64_t turn_step(double freq) {
   return bits >> 63 ? 0 - r : r;
 }
 
+// Sine and cosine of u * 2^-32 turns: an eighth of a turn to either side of a quarter's multiple, by the Taylor
+// series (the first terms left out are below 2e-9 and 2e-10), then turned by the quarters.
+__device__ __forceinline__ void sincos_turns(uint32_t u, float* sine, float* cosine) {
+  const uint32_t quarters = (u + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(u - (quarters << 30))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float y = x * x;
+  float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(s, y, 1.0f / 120.0f);
+  s = fmaf(s, y, -1.0f / 6.0f);
+  s = fmaf(s * y, x, x);
+  float c = fmaf(y, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  c = fmaf(c, y, -1.0f / 720.0f);
+  c = fmaf(c, y, 1.0f / 24.0f);
+  c = fmaf(c, y, -0.5f);
+  c = fmaf(c, y, 1.0f);
+  const bool odd = (quarters & 1u) != 0;
+  const float a = odd ? c : s, b = odd ? s : c;
+  *sine = (quarters & 2u) != 0 ? -a : a;
+  *cosine = ((quarters + 1u) & 2u) != 0 ? -b : b;
+}
+
 // V: values of one access. kHalf: the layout. A piece that turns is V pairs (half layout, two
 // accesses) or V / 2 pairs (interleaved, one access; one pair and two accesses at V = 1).
 template <typename T, int V, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const RotaryParams p) {
   constexpr bool kTwo = kHalf || V == 1;
   constexpr int kPairs = kTwo ? V : V / 2;
   __shared__ __align__(16) float cosines[kMaxAngles], sines[kMaxAngles];
@@ -65,106 +87,88 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams 
   const uint32_t tokens = min(p.tile_tokens, p.tokens - t0);
   const uint32_t first_pair = segment * p.pairs.d, pairs = min(p.pairs.d, p.all_pairs - first_pair);
 
-  for (uint32_t i = threadIdx.x; i < tokens * p.pairs.d; i += kThreads) {
-    const uint32_t t = quotient(p.pairs, i), k = i - t * p.pairs.d;
-    if (k < pairs) {
-      const int64_t pos = p.positions[t0 + t];
-      const uint64_t phase = static_cast<uint64_t>(pos) * turn_step(p.freqs[first_pair + k]);
-      // top 32 bits, signed: half turns in [-1, 1)
-      const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      float s, c;
-      sincospif(half_turns, &s, &c);
-      cosines[i] = c * p.scale;
-      sines[i] = s * p.scale * p.sign;
-    }
-  }
-  __syncthreads();
-
   using P = Pack<T, V>;
   const T* const x = static_cast<const T*>(p.x) + t0 * p.x_ts + h0 * p.x_hs;
   T* const out = static_cast<T*>(p.out) + t0 * p.out_ts + h0 * p.out_hs;
   const uint32_t rows = tokens * heads;
-  // Row r of the tile is head r / tokens of token r % tokens where tokens lie closer, and the other way round;
-  // here heads are the inner axis: neighbouring pieces of a token's heads.
+  // row r of the tile: token t, and the head that is returned
   auto place = [&](uint32_t r, uint32_t* t) {
     *t = heads == p.tile_heads.d ? quotient(p.tile_heads, r) : r / heads;
     return r - *t * heads;
   };
-
   const uint32_t turning = rows * p.turn_items.d;
-  for (uint32_t u0 = threadIdx.x; u0 < turning; u0 += kThreads * kAhead) {
-    P a[kAhead], b[kAhead];
-    uint32_t angle[kAhead];
-    T* dst[kAhead];
+  P a, b;
+  uint32_t angle = 0;
+  T* dst = nullptr;
+  auto load = [&](uint32_t u) {
+    dst = nullptr;
+    if (u >= turning) return;
+    const uint32_t r = quotient(p.turn_items, u), first = (u - r * p.turn_items.d) * kPairs;
+    if (first >= pairs) return;
+    uint32_t t;
+    const uint32_t h = place(r, &t);
+    angle = t * p.pairs.d + first;
+    const uint32_t col = p.start + (kHalf ? 1 : 2) * (first_pair + first);
+    const T* src = x + t * p.x_ts + h * p.x_hs + col;
+    dst = out + t * p.out_ts + h * p.out_hs + col;
+    a = *reinterpret_cast<const P*>(src);
+    if constexpr (kTwo) b = *reinterpret_cast<const P*>(src + (kHalf ? p.all_pairs : 1));
+  };
+  load(threadIdx.x);  // on its way while the angles are computed
+
+  uint32_t last_pair = 0xffffffffu;
+  uint64_t step = 0;
+  for (uint32_t i = threadIdx.x; i < tokens * p.pairs.d; i += kThreads) {
+    const uint32_t t = quotient(p.pairs, i), k = i - t * p.pairs.d;
+    if (k >= pairs) continue;
+    if (k != last_pair) step = turn_step(p.freqs[first_pair + k]);  // mostly one for all of a thread's tokens
+    last_pair = k;
+    const int64_t pos = p.positions[t0 + t];
+    float s, c;
+    sincos_turns(static_cast<uint32_t>(static_cast<uint64_t>(pos) * step >> 32), &s, &c);
+    cosines[i] = c * p.scale;
+    sines[i] = s * p.scale * p.sign;
+  }
+  __syncthreads();
+
+  for (uint32_t u = threadIdx.x; u < turning; u += kThreads) {
+    if (u != threadIdx.x) load(u);
+    if (dst == nullptr) continue;
+    float c[kPairs], s[kPairs];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const uint32_t u = u0 + k * kThreads;
-      dst[k] = nullptr;
-      if (u < turning) {
-        const uint32_t r = quotient(p.turn_items, u), first = (u - r * p.turn_items.d) * kPairs;
-        if (first < pairs) {
-          uint32_t t;
-          const uint32_t h = place(r, &t);
-          angle[k] = t * p.pairs.d + first;
-          const uint32_t col = p.start + (kHalf ? 1 : 2) * (first_pair + first);
-          const T* src = x + t * p.x_ts + h * p.x_hs + col;
-          dst[k] = out + t * p.out_ts + h * p.out_hs + col;
-          a[k] = *reinterpret_cast<const P*>(src);
-          if constexpr (kTwo) b[k] = *reinterpret_cast<const P*>(src + (kHalf ? p.all_pairs : 1));
-        }
+    for (int i = 0; i < kPairs; i += kPairs % 4 == 0 ? 4 : 1) {
+      if constexpr (kPairs % 4 == 0) {
+        const float4 fc = *reinterpret_cast<const float4*>(&cosines[angle + i]);
+        const float4 fs = *reinterpret_cast<const float4*>(&sines[angle + i]);
+        c[i] = fc.x, c[i + 1] = fc.y, c[i + 2] = fc.z, c[i + 3] = fc.w;
+        s[i] = fs.x, s[i + 1] = fs.y, s[i + 2] = fs.z, s[i + 3] = fs.w;
+      } else {
+        c[i] = cosines[angle + i];
+        s[i] = sines[angle + i];
       }
     }
+    P ya, yb;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (dst[k] == nullptr) continue;
-      float c[kPairs], s[kPairs];
-#pragma unroll
-      for (int i = 0; i < kPairs; i += kPairs % 4 == 0 ? 4 : 1) {
-        if constexpr (kPairs % 4 == 0) {
-          const float4 fc = *reinterpret_cast<const float4*>(&cosines[angle[k] + i]);
-          const float4 fs = *reinterpret_cast<const float4*>(&sines[angle[k] + i]);
-          c[i] = fc.x, c[i + 1] = fc.y, c[i + 2] = fc.z, c[i + 3] = fc.w;
-          s[i] = fs.x, s[i + 1] = fs.y, s[i + 2] = fs.z, s[i + 3] = fs.w;
-        } else {
-          c[i] = cosines[angle[k] + i];
-          s[i] = sines[angle[k] + i];
-        }
-      }
-      P ya, yb;
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const float fa = to_float(kTwo ? a[k].v[i] : a[k].v[2 * i]);
-        const float fb = to_float(kTwo ? b[k].v[i] : a[k].v[2 * i + 1]);
-        (kTwo ? ya.v[i] : ya.v[2 * i]) = from_float<T>(fmaf(fa, c[i], -fb * s[i]));
-        (kTwo ? yb.v[i] : ya.v[2 * i + 1]) = from_float<T>(fmaf(fa, s[i], fb * c[i]));
-      }
-      *reinterpret_cast<P*>(dst[k]) = ya;
-      if constexpr (kTwo) *reinterpret_cast<P*>(dst[k] + (kHalf ? p.all_pairs : 1)) = yb;
+    for (int i = 0; i < kPairs; ++i) {
+      const float fa = to_float(kTwo ? a.v[i] : a.v[2 * i]);
+      const float fb = to_float(kTwo ? b.v[i] : a.v[2 * i + 1]);
+      (kTwo ? ya.v[i] : ya.v[2 * i]) = from_float<T>(fmaf(fa, c[i], -fb * s[i]));
+      (kTwo ? yb.v[i] : ya.v[2 * i + 1]) = from_float<T>(fmaf(fa, s[i], fb * c[i]));
     }
+    *reinterpret_cast<P*>(dst) = ya;
+    if constexpr (kTwo) *reinterpret_cast<P*>(dst + (kHalf ? p.all_pairs : 1)) = yb;
   }
 
   if (segment != 0) return;
-  const uint32_t copying = p.copy_items.d == 0 ? 0 : rows * p.copy_items.d;
-  for (uint32_t u0 = threadIdx.x; u0 < copying; u0 += kThreads * kAhead) {
-    P a[kAhead];
-    T* dst[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const uint32_t u = u0 + k * kThreads;
-      dst[k] = nullptr;
-      if (u < copying) {
-        const uint32_t r = quotient(p.copy_items, u);
-        int col = static_cast<int>(u - r * p.copy_items.d) * V;
-        if (col >= p.start) col += 2 * p.all_pairs;
-        uint32_t t;
-        const uint32_t h = place(r, &t);
-        a[k] = *reinterpret_cast<const P*>(x + t * p.x_ts + h * p.x_hs + col);
-        dst[k] = out + t * p.out_ts + h * p.out_hs + col;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (dst[k] != nullptr) *reinterpret_cast<P*>(dst[k]) = a[k];
+  const uint32_t copying = rows * p.copy_items.d;
+  for (uint32_t u = threadIdx.x; u < copying; u += kThreads) {
+    const uint32_t r = quotient(p.copy_items, u);
+    int col = static_cast<int>(u - r * p.copy_items.d) * V;
+    if (col >= p.start) col += 2 * p.all_pairs;
+    uint32_t t;
+    const uint32_t h = place(r, &t);
+    *reinterpret_cast<P*>(out + t * p.out_ts + h * p.out_hs + col) =
+        *reinterpret_cast<const P*>(x + t * p.x_ts + h * p.x_hs + col);
   }
 }
 
@@ -181,14 +185,20 @@ cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half
   const int64_t segments = (p.all_pairs + kMaxAngles - 1) / kMaxAngles;
   const int64_t pairs = segments > 1 ? kMaxAngles : p.all_pairs;
   const int64_t turn_items = pairs / pairs_of_item, copy_items = in_place ? 0 : (dim - 2 * p.all_pairs) / v;
-  // Pieces of a CTA: eight for each thread where the chip has enough of them to do, one otherwise. All heads of one
-  // or more tokens, or a part of one token's heads.
-  const int64_t row = turn_items + copy_items, total = tokens * p.heads * row;
-  const int64_t pieces = total >= int64_t(sms) * 2048 ? 8 * kThreads : total >= int64_t(sms) * 1024 ? 4 * kThreads : kThreads;
+  // A CTA owns all heads of some tokens, or a part of one token's heads: from one piece to about eight for each
+  // thread, in whole rounds of the CTAs that the chip holds (a last round of a few CTAs takes as long as a full one).
+  const int64_t row = turn_items + copy_items, total = tokens * p.heads * row, slots = int64_t(sms) * kResident;
+  const int64_t rounds = (total + slots * 8 * kThreads - 1) / (slots * 8 * kThreads);
+  int64_t pieces = total / (slots * rounds);
+  if (pieces < kThreads) pieces = kThreads;
   int64_t heads = pieces / row < 1 ? 1 : pieces / row < p.heads ? pieces / row : p.heads;
   const int64_t head_tiles = (p.heads + heads - 1) / heads;
   heads = (p.heads + head_tiles - 1) / head_tiles;
-  int64_t tile_tokens = heads == p.heads ? pieces / (row * heads) : 1;
+  int64_t tile_tokens = 1;
+  if (heads == p.heads) {
+    tile_tokens = (tokens + slots * rounds - 1) / (slots * rounds);
+    if (tile_tokens * heads * row < kThreads) tile_tokens = kThreads / (heads * row);
+  }
   if (tile_tokens > kMaxAngles / pairs) tile_tokens = kMaxAngles / pairs;
   if (tile_tokens < 1) tile_tokens = 1;
   p.tile_tokens = static_cast<int32_t>(tile_tokens);
