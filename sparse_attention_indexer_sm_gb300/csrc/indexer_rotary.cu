@@ -7,7 +7,8 @@
 //   one integer product; position * fraction wraps modulo one turn by itself, without any
 //   rounding, and its top 32 bits are the angle.
 // - The split. A CTA owns a tile of tokens and heads. Its threads first leave the tile's sines and cosines
-//   in shared memory, each computed once, then walk over the rows in 16-byte pieces. Many small CTAs
+//   in shared memory, each computed once, then walk over the rows in pieces of 32 bytes (interleaved) or twice 16 (half layout; twice 32 needs too
+//   many registers). Many small CTAs
 //   hide the loads' latency better than several pieces in flight in each thread (one piece and six CTAs an SM
 //   against two and five: 8192 x 64 x 128 in bf16, half of each row turned, 48 against 52 us). Sines kept in registers over a thread's heads took up to 232
 //   registers and left the loads' latency bare (8192 x 64 x 128 in bf16, half of each row turned: 89 us).
@@ -18,7 +19,9 @@ namespace indexer_gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kResident = 6;       // CTAs of an SM
+
+// CTAs of an SM: what registers allow of pieces of 32 bytes, or of two accesses of 16 bytes each.
+constexpr int resident(int bytes) { return bytes == 32 ? 5 : 6; }
 constexpr int kMaxAngles = 2048;   // sines of a tile
 
 struct RotaryParams {
@@ -73,7 +76,7 @@ __device__ __forceinline__ void sincos_turns(uint32_t u, float* sine, float* cos
 // V: values of one access. kHalf: the layout. A piece that turns is V pairs (half layout, two
 // accesses) or V / 2 pairs (interleaved, one access; one pair and two accesses at V = 1).
 template <typename T, int V, bool kHalf>
-__global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, resident(V * sizeof(T))) rotary_kernel(const RotaryParams p) {
   constexpr bool kTwo = kHalf || V == 1;
   constexpr int kPairs = kTwo ? V : V / 2;
   __shared__ __align__(16) float cosines[kMaxAngles], sines[kMaxAngles];
@@ -87,7 +90,9 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const Rotar
   const uint32_t tokens = min(p.tile_tokens, p.tokens - t0);
   const uint32_t first_pair = segment * p.pairs.d, pairs = min(p.pairs.d, p.all_pairs - first_pair);
 
-  using P = Pack<T, V>;
+  struct alignas(sizeof(T) * V) P {
+    T v[V];
+  };
   const T* const x = static_cast<const T*>(p.x) + t0 * p.x_ts + h0 * p.x_hs;
   T* const out = static_cast<T*>(p.out) + t0 * p.out_ts + h0 * p.out_hs;
   const uint32_t rows = tokens * heads;
@@ -175,19 +180,19 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const Rotar
 template <typename T>
 cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half, bool in_place, int sms,
                           cudaStream_t stream) {
-  // 16-byte accesses where every row, and the pairs' two halves, start on 16 bytes
-  constexpr int kV = 16 / sizeof(T);
+  // The widest accesses on whose boundaries every row starts, and the turned columns' parts: 32 bytes (interleaved
+  // only: 8191 x 64 x 128 in bf16 46 us against 52 with 16 bytes), 16, or single values.
   const int64_t all = p.x_ts | p.x_hs | p.out_ts | p.out_hs | dim | p.start | (half ? p.all_pairs : 2 * p.all_pairs);
-  const bool wide = all % kV == 0 &&
-                    ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15u) == 0;
-  const int v = wide ? kV : 1;
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out);
+  constexpr int kV = 16 / sizeof(T);
+  const int v = !half && all % (2 * kV) == 0 && (bases & 31u) == 0 ? 2 * kV : all % kV == 0 && (bases & 15u) == 0 ? kV : 1;
   const int pairs_of_item = half || v == 1 ? v : v / 2;
   const int64_t segments = (p.all_pairs + kMaxAngles - 1) / kMaxAngles;
   const int64_t pairs = segments > 1 ? kMaxAngles : p.all_pairs;
   const int64_t turn_items = pairs / pairs_of_item, copy_items = in_place ? 0 : (dim - 2 * p.all_pairs) / v;
   // A CTA owns all heads of some tokens, or a part of one token's heads: from one piece to about eight for each
   // thread, in whole rounds of the CTAs that the chip holds (a last round of a few CTAs takes as long as a full one).
-  const int64_t row = turn_items + copy_items, total = tokens * p.heads * row, slots = int64_t(sms) * kResident;
+  const int64_t row = turn_items + copy_items, total = tokens * p.heads * row, slots = int64_t(sms) * resident(v * sizeof(T));
   const int64_t rounds = (total + slots * 8 * kThreads - 1) / (slots * 8 * kThreads);
   int64_t pieces = total / (slots * rounds);
   if (pieces < kThreads) pieces = kThreads;
@@ -216,7 +221,9 @@ cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half
     p.tokens = static_cast<int32_t>(n);
     const unsigned grid = static_cast<unsigned>((n + tile_tokens - 1) / tile_tokens * head_tiles * segments);
     cudaError_t e;
-    if (wide)
+    if (v == 2 * kV)
+      e = launch(rotary_kernel<T, 2 * kV, false>, grid, kThreads, 0, stream, p);
+    else if (v == kV)
       e = half ? launch(rotary_kernel<T, kV, true>, grid, kThreads, 0, stream, p)
                : launch(rotary_kernel<T, kV, false>, grid, kThreads, 0, stream, p);
     else
