@@ -2,7 +2,9 @@
 
 Every object is compiled for sm_103a only, all of them in parallel, then linked
 against the shared CUDA runtime (so that the process keeps a single runtime
-together with PyTorch). Run ``python -m sparse_attention_indexer_sm_gb300.build``.
+together with PyTorch). Beside it stands the indexer operators' Python binding, a
+C++ module for this interpreter and this PyTorch, linked against the library. Run
+``python -m sparse_attention_indexer_sm_gb300.build``.
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +31,7 @@ KERNEL_OBJECTS = [(f"topk_select_{cta}_{form}", ["-DTOPK_CTA_THREADS=%d" % cta, 
 KERNEL_OBJECTS += [(f"topk_select_{cta}", ["-DTOPK_CTA_THREADS=%d" % cta]) for cta in (512, 256)]
 HEADERS = (os.path.join(CSRC, "topk_select.cuh"), os.path.join(CSRC, "indexer_common.cuh"),
            os.path.join(INCLUDE, "topk_transform.h"), os.path.join(INCLUDE, "indexer_ops.h"))
+BINDING_SOURCE = os.path.join(CSRC, "indexer_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I" + INCLUDE, "-I" + CSRC]
@@ -40,12 +44,42 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
+def binding_path() -> str:
+    """The binding's module, of this PyTorch's version."""
+    import torch
+    return os.path.join(BUILD_DIR, f"indexer_binding-{torch.__version__}.so")
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    outs = [LIB_PATH, binding_path()]
+    if not all(os.path.exists(p) for p in outs):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + list(HEADERS) + [__file__]
+    t = min(os.path.getmtime(p) for p in outs)
+    deps = [os.path.join(CSRC, s) for s in SOURCES] + list(HEADERS) + [BINDING_SOURCE, __file__]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _binding_commands(obj: str, out: str, cuda_home: str) -> tuple[list[str], list[str]]:
+    """The host compiler's commands for the binding: compile, link."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SOURCE, "-o", obj,
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                "-isystem", os.path.join(base, "include"),
+                "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda_home, "include"),
+                "-isystem", sysconfig.get_paths()["include"], "-I" + INCLUDE]
+    link = [cxx, "-shared", "-o", out, obj, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch",
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + BUILD_DIR, "-ltopk_transform",
+            "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
+def _run(cmd: list[str], what: str) -> None:
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed ({' '.join(cmd)}):\n{r.stdout}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -54,31 +88,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     exe = nvcc()
+    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(exe)))
     procs, objs = [], []
     units = [(name, defs, "topk_select.cu") for name, defs in KERNEL_OBJECTS]
     units += [(os.path.splitext(src)[0], [], src) for src in SOURCES[1:]]
+
+    def start(cmd):
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+
     for name, defs, src in units:
         obj = os.path.join(BUILD_DIR, name + ".o")
         cmd = [exe, *NVCC_FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                            text=True)))
+        start(cmd)
         objs.append(obj)
+    binding = binding_path()
+    binding_tmp = binding + f".{os.getpid()}.tmp"
+    compile_binding, link_binding = _binding_commands(os.path.join(BUILD_DIR, "indexer_binding.o"), binding_tmp,
+                                                      cuda_home)
+    start(compile_binding)
     for cmd, p in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
-            raise RuntimeError(f"nvcc failed ({' '.join(cmd)}):\n{out}")
+            raise RuntimeError(f"compiler failed ({' '.join(cmd)}):\n{out}")
         if verbose and out:
             print(out, file=sys.stderr)
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cuda_lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(exe))), "lib64")
-    link = [exe, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + cuda_lib,
-            "-o", tmp, *objs]
-    r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed ({' '.join(link)}):\n{r.stdout}")
+    cuda_lib = os.path.join(cuda_home, "lib64")
+    _run([exe, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + cuda_lib,
+          "-Xlinker", "-soname,libtopk_transform.so", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB_PATH)
+    _run(link_binding, "link of the binding")
+    os.replace(binding_tmp, binding)
     return LIB_PATH
 
 

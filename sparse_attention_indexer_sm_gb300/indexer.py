@@ -1,9 +1,9 @@
 """The operators around the top-k of a sparse-attention indexer.
 
 A thin binding over the C ABI in ``include/indexer_ops.h``, in the manner of the
-package's top-k calls: tensors are checked and marshalled, the work runs in the
-library's sm_103a kernels on the tensors' device and the current torch stream (or
-``stream``), and nothing falls back to torch. A decode step, with a paged cache
+package's top-k calls: tensors are checked and marshalled (in ``csrc/indexer_binding.cpp``),
+the work runs in the library's sm_103a kernels on the tensors' device and the current torch
+stream (or ``stream``), and nothing falls back to torch. A decode step, with a paged cache
 ``codes`` [pages, page_size, 128] (float8_e4m3fn) and ``scales`` [pages, page_size, 1]:
 
     freqs, scale = indexer_rotary_freqs(64, device="cuda")
@@ -19,11 +19,14 @@ library's sm_103a kernels on the tensors' device and the current torch stream (o
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
+import os
 
 import torch
 
-from . import _check, load_library
+from . import TopkError, _build, _check, load_library
 
 __all__ = [
     "indexer_rotary", "indexer_rotary_freqs", "indexer_quantise", "indexer_cache_write",
@@ -37,6 +40,25 @@ INDEXER_MAX_HEADS = 128
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _FORMATS = {"fp32": 0, "pow2": 1}
+
+_binding = None
+
+
+def _load_binding():
+    """The compiled binding (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        load_library()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first (python -m "
+                               "sparse_attention_indexer_sm_gb300.build, or __graft_entry__.build())")
+        loader = importlib.machinery.ExtensionFileLoader("indexer_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("indexer_binding", loader))
+        loader.exec_module(module)
+        module.set_error(TopkError)
+        _binding = module
+    return _binding
 
 
 class IndexerCache(ctypes.Structure):
@@ -70,92 +92,19 @@ def declare(lib: ctypes.CDLL) -> None:
         raise RuntimeError("indexer_cache_t layout differs between the library and this binding")
 
 
-# ---------------------------------------------------------------- checks and the call
-
-def _tensor(t, name: str, dtypes, device=None) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (the library has no CPU path)")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-_INT32, _FP32, _FP64, _E4M3 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.float8_e4m3fn,)
-
-
-def _contiguous(t, name: str, dtypes, shape, device) -> None:
-    _tensor(t, name, dtypes, device)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor of shape {tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
-
-
-def _rows(x, name: str):
-    """(tokens, heads, dim, token stride, head stride) of a [tokens, dim] or
-    [tokens, heads, dim] tensor with unit column stride."""
-    _tensor(x, name, _DTYPES)
-    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
-        raise ValueError(f"{name} must be [tokens, dim] or [tokens, heads, dim] with unit inner stride")
-    if x.dim() == 2:
-        return x.shape[0], 1, x.shape[1], x.stride(0), 0
-    return x.shape[0], x.shape[1], x.shape[2], x.stride(0), x.stride(1)
-
-
 def _choice(value, table, name: str) -> int:
     if value not in table:
         raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, got {value!r}")
     return table[value]
 
 
-def _call(what: str, device, stream, *args) -> None:
-    fn = getattr(load_library(), what)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, s.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, s.cuda_stream)
-    if st != 0:
-        _check(st, what)
-
-
-def _fresh(shape, dtype, device, stream):
-    """An output of this call: in use on `stream`, where one is given, until the call's
-    kernel has ended."""
-    out = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        out.record_stream(stream)
+def _on(stream, call, given, *args):
+    """A call on a stream of the caller's: outputs made by it are in use there until its kernel has ended."""
+    out = call(*args, stream.cuda_stream)
+    for t, g in zip(out if isinstance(out, tuple) else (out,), given):
+        if g is None:
+            t.record_stream(stream)
     return out
-
-
-def _cache(codes, scales, device=None) -> IndexerCache:
-    _tensor(codes, "codes", _E4M3, device)
-    device = codes.device
-    _tensor(scales, "scales", _FP32, device)
-    if codes.dim() != 3 or codes.shape[2] < 1 or (codes.shape[2] > 1 and codes.stride(2) != 1):
-        raise ValueError("codes must be [pages, page_size, dim] with unit inner stride")
-    pages, size, dim = codes.shape
-    nb = -(-dim // INDEXER_BLOCK)
-    if tuple(scales.shape) != (pages, size, nb) or (nb > 1 and scales.stride(2) != 1):
-        raise ValueError(f"scales must be [{pages}, {size}, {nb}] (one for each {INDEXER_BLOCK} columns) "
-                         "with unit inner stride")
-    if size < 1:
-        raise ValueError("a page must hold at least one row")
-    if pages * size > 2**31 - 1:
-        raise ValueError("a cache holds at most 2**31 - 1 rows")
-    c = IndexerCache(codes.data_ptr(), scales.data_ptr(), pages, codes.stride(0), codes.stride(1),
-                     scales.stride(0), scales.stride(1), size, dim)
-    for t, name, width in ((codes, "codes", dim), (scales, "scales", nb)):
-        # rows apart from each other: pages outside rows, or rows outside pages
-        axes = sorted((t.stride(i), t.shape[i]) for i in (0, 1) if t.shape[i] > 1)
-        for stride, count in axes:
-            if stride < width:
-                raise ValueError(f"{name}: rows must not overlap")
-            width += (count - 1) * stride
-    return c
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -193,36 +142,6 @@ def indexer_rotary_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | 
     return freqs.to(device), scale
 
 
-def _rotary(x, positions, freqs, layout, start, scale, transpose, out, stream):
-    tokens, heads, dim, ts, hs = _rows(x, "x")
-    if out is None:
-        out = _fresh(x.shape, x.dtype, x.device, stream)
-    ots, ohs = out.stride(0), out.stride(1) if x.dim() == 3 else 0
-    _call("indexer_rotary", x.device, stream, x.data_ptr(), ts, hs, positions.data_ptr(),
-          freqs.data_ptr(), _DTYPES[x.dtype], tokens, heads, dim, 2 * freqs.shape[0], start, layout,
-          scale, transpose, out.data_ptr(), ots, ohs)
-    return out
-
-
-class _Rotary(torch.autograd.Function):
-    """The rotation is linear in x: its gradient is the transposed rotation, by this same function."""
-
-    @staticmethod
-    def forward(ctx, x, positions, freqs, layout, start, scale, transpose):
-        ctx.save_for_backward(positions, freqs)
-        ctx.how = layout, start, scale, transpose
-        return _rotary(x, positions, freqs, layout, start, scale, transpose, None, None)
-
-    @staticmethod
-    def backward(ctx, grad):
-        positions, freqs = ctx.saved_tensors
-        layout, start, scale, transpose = ctx.how
-        if grad.shape[-1] > 1 and grad.stride(-1) != 1:
-            grad = grad.contiguous()
-        grad = _Rotary.apply(grad, positions, freqs, layout, start, scale, not transpose)
-        return grad, None, None, None, None, None, None
-
-
 def indexer_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *,
                    layout: str = "half", start: int = 0, scale: float = 1.0,
                    transpose: bool = False, out: torch.Tensor | None = None,
@@ -236,41 +155,11 @@ def indexer_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor
     their precision at any position. transpose: the rotation of a gradient (by the opposite
     angle, with the same scale). out: a tensor like x, or x itself for a call in place.
     Differentiable in x (twice too); a call with `out` or `stream` is not."""
+    f = (_binding or _load_binding()).rotary
     how = _choice(layout, _LAYOUTS, "layout")
-    tokens, _, dim, _, _ = _rows(x, "x")
-    _tensor(positions, "positions", _INT32, x.device)
-    if positions.dim() != 1 or positions.shape[0] != tokens or (tokens > 1 and positions.stride(0) != 1):
-        raise ValueError(f"positions must be a contiguous int32 vector of length {tokens}")
-    _tensor(freqs, "freqs", _FP64, x.device)
-    if freqs.dim() != 1 or freqs.shape[0] < 1 or (freqs.shape[0] > 1 and freqs.stride(0) != 1):
-        raise ValueError("freqs must be a contiguous fp64 vector of at least one frequency")
-    start = int(start)
-    if start < 0 or start + 2 * freqs.shape[0] > dim:
-        raise ValueError(f"columns [{start}, {start + 2 * freqs.shape[0]}) do not lie within the row of {dim}")
-    if torch.is_grad_enabled() and x.requires_grad:
-        if out is not None or stream is not None:
-            raise ValueError("a differentiable call takes neither out nor stream")
-        return _Rotary.apply(x, positions, freqs, how, start, float(scale), bool(transpose))
-    if out is not None:
-        _tensor(out, "out", (x.dtype,), x.device)
-        if out.shape != x.shape or (dim > 1 and out.stride(-1) != 1):
-            raise ValueError(f"out must have x's shape {tuple(x.shape)} and unit inner stride")
-        if torch.is_grad_enabled() and out.requires_grad:
-            raise ValueError("out must not require a gradient")
-        if _overlap(x, out) and not (out.data_ptr() == x.data_ptr() and out.stride() == x.stride()):
-            raise ValueError("out must be x itself or not overlap it")
-    return _rotary(x, positions, freqs, how, start, float(scale), bool(transpose), out, stream)
-
-
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the spans of memory of two tensors meet."""
-    def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+    if stream is not None:
+        return _on(stream, f, (out,), x, positions, freqs, how, start, scale, transpose, out)
+    return f(x, positions, freqs, how, start, scale, transpose, out, None)
 
 
 # ---------------------------------------------------------------- 8-bit rows and cache
@@ -285,28 +174,11 @@ def indexer_quantise(x: torch.Tensor, *, scale_format: str = "fp32",
     [tokens, heads] (or [tokens]), for rows of one block: scales then holds
     weights * scale, of the same shape, as indexer_scores takes it. A block that holds an
     infinity or a NaN becomes NaN throughout. codes, scales: contiguous outputs."""
+    f = (_binding or _load_binding()).quantise
     fmt = _choice(scale_format, _FORMATS, "scale_format")
-    tokens, heads, dim, ts, hs = _rows(x, "x")
-    if dim < 1:
-        raise ValueError("rows must have at least one column")
-    nb = -(-dim // INDEXER_BLOCK)
-    dev = x.device
-    if weights is not None:
-        if nb != 1:
-            raise ValueError(f"weights need rows of one block (at most {INDEXER_BLOCK} columns), got {dim}")
-        _contiguous(weights, "weights", _FP32, x.shape[:-1], dev)
-    scale_shape = x.shape[:-1] if weights is not None else (*x.shape[:-1], nb)
-    if codes is None:
-        codes = _fresh(x.shape, torch.float8_e4m3fn, dev, stream)
-    else:
-        _contiguous(codes, "codes", _E4M3, x.shape, dev)
-    if scales is None:
-        scales = _fresh(scale_shape, torch.float32, dev, stream)
-    else:
-        _contiguous(scales, "scales", _FP32, scale_shape, dev)
-    _call("indexer_quantise", dev, stream, x.data_ptr(), ts, hs, _DTYPES[x.dtype], tokens, heads, dim,
-          fmt, None if weights is None else weights.data_ptr(), codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    if stream is not None:
+        return _on(stream, f, (codes, scales), x, fmt, weights, codes, scales)
+    return f(x, fmt, weights, codes, scales, None)
 
 
 def indexer_cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor,
@@ -316,18 +188,9 @@ def indexer_cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tenso
     float8_e4m3fn, scales [pages, page_size, ceil(dim / 128)] fp32 (views of one buffer are
     fine). Slot -1: the row is not written. Another slot outside the cache is not written
     either, and counted (indexer_guard_hits). Slots should differ from each other."""
+    f = (_binding or _load_binding()).cache_write
     fmt = _choice(scale_format, _FORMATS, "scale_format")
-    tokens, _, dim, ts, _ = _rows(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [tokens, dim]")
-    cache = _cache(codes, scales, x.device)
-    if dim != cache.dim:
-        raise ValueError(f"x has rows of {dim} columns, the cache {cache.dim}")
-    _tensor(slots, "slots", _INT32, x.device)
-    if slots.dim() != 1 or slots.shape[0] != tokens or (tokens > 1 and slots.stride(0) != 1):
-        raise ValueError(f"slots must be a contiguous int32 vector of length {tokens}")
-    _call("indexer_cache_write", x.device, stream, x.data_ptr(), ts, _DTYPES[x.dtype], tokens,
-          slots.data_ptr(), fmt, ctypes.addressof(cache))
+    f(x, slots, codes, scales, fmt, None if stream is None else stream.cuda_stream)
 
 
 def indexer_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, *,
@@ -336,20 +199,11 @@ def indexer_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.T
     """The cache rows at `slots` (int32, contiguous, any shape; the positions that
     topk_transform_paged writes are such slots) as `dtype`: [*slots.shape, dim]. Slot -1
     gives zeros; another slot outside the cache too, and is counted (indexer_guard_hits)."""
+    f = (_binding or _load_binding()).cache_read
     kind = _choice(dtype, _DTYPES, "dtype")
-    cache = _cache(codes, scales)
-    dev = codes.device
-    _tensor(slots, "slots", _INT32, dev)
-    if not slots.is_contiguous():
-        raise ValueError("slots must be contiguous")
-    shape = (*slots.shape, cache.dim)
-    if out is None:
-        out = _fresh(shape, dtype, dev, stream)
-    else:
-        _contiguous(out, "out", (dtype,), shape, dev)
-    _call("indexer_cache_read", dev, stream, ctypes.addressof(cache), slots.data_ptr(), slots.numel(),
-          kind, out.data_ptr())
-    return out
+    if stream is not None:
+        return _on(stream, f, (out,), codes, scales, slots, kind, out)
+    return f(codes, scales, slots, kind, out, None)
 
 
 # ---------------------------------------------------------------- scores
@@ -368,42 +222,10 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, 
     [pages, page_size, 128] and scales [pages, page_size, 1]; page_table int32 [batch, P]
     with P * page_size >= row_len; seq_lens int32 [batch, queries]. Positions on a page
     outside the cache get -inf and are counted (indexer_guard_hits)."""
-    _tensor(q, "q", _E4M3)
-    dev = q.device
-    if q.dim() != 4 or q.shape[3] != INDEXER_BLOCK or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous [batch, queries, heads, {INDEXER_BLOCK}] tensor")
-    batch, queries, heads, _ = q.shape
-    if not 1 <= heads <= INDEXER_MAX_HEADS:
-        raise ValueError(f"heads must be in [1, {INDEXER_MAX_HEADS}], got {heads}")
-    _contiguous(weights, "weights", _FP32, (batch, queries, heads), dev)
-    cache = _cache(codes, scales, dev)
-    if cache.dim != INDEXER_BLOCK:
-        raise ValueError(f"the cache's rows must have {INDEXER_BLOCK} columns, got {cache.dim}")
-    if (q.data_ptr() | codes.data_ptr() | (codes.stride(0) if codes.shape[0] > 1 else 0)
-            | (codes.stride(1) if codes.shape[1] > 1 else 0)) % 16:
-        raise ValueError("q and every row of codes must start on 16 bytes")
-    row_len = int(row_len)
-    if not 1 <= row_len <= 2**31 - 1:
-        raise ValueError(f"row_len must be in [1, 2**31 - 1], got {row_len}")
-    _tensor(page_table, "page_table", _INT32, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != batch or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [batch, pages] int32 with unit inner stride")
-    if page_table.shape[1] * cache.page_size < row_len:
-        raise ValueError("page_table has too few pages for the rows")
-    pt_stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
-    if pt_stride < page_table.shape[1]:
-        raise ValueError("page_table rows must not overlap (use .contiguous() on expanded tables)")
-    _contiguous(seq_lens, "seq_lens", _INT32, (batch, queries), dev)
-    shape = (batch * queries, row_len)
-    if out is None:
-        out = _fresh(shape, torch.float32, dev, stream)
-    else:
-        _contiguous(out, "out", _FP32, shape, dev)
-    _call("indexer_scores", dev, stream, q.data_ptr(), weights.data_ptr(), ctypes.addressof(cache),
-          page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), batch, queries, heads, row_len,
-          out.data_ptr())
-    return out
+    f = (_binding or _load_binding()).scores
+    if stream is not None:
+        return _on(stream, f, (out,), q, weights, codes, scales, page_table, seq_lens, row_len, out)
+    return f(q, weights, codes, scales, page_table, seq_lens, row_len, out, None)
 
 
 def indexer_guard_hits() -> int:
