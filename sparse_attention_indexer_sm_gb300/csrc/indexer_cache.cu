@@ -4,11 +4,11 @@
 // Bound by memory: each element is read once and written once, so few operations may be spent on one.
 // - Rounding. A code is the e4m3 value nearest to the real quotient x / scale. x times an approximate
 //   1 / scale, a little too small and a little too large, gives two codes with one instruction for
-//   each pair; where they agree, the code is that, and almost everywhere they do. A lane in which one
-//   pair differs takes each value's remainder, which one fma gives exactly, as a sticky last bit: the
-//   quotient rounded to odd, which rounds to e4m3 as the real one does. With a power of two as the
-//   scale the quotient is exact already.
-// - The split. Eight lanes own a block, 16 values each, two blocks in flight in each lane: with sixteen lanes of 8
+//   each pair; where they agree, the code is that, and almost everywhere they do. Where they do not, a 16-bit
+//   value lies on a border between codes up to the scale's own rounding, whose sign decides. A 32-bit
+//   value's remainder, which one fma gives exactly, becomes a sticky last bit: the quotient rounded to
+//   odd, which rounds to e4m3 as the real one does. With a power of two as the scale the quotient is exact.
+// - The split. Eight lanes own a block, 16 values each: with sixteen lanes of 8
 //   values what a lane does once a block (its place, its scale) cost as much as its values, and the kernel
 //   was bound by instructions (8192 x 64 rows of 128 in bf16: 60 us). The largest magnitude is
 //   found on the bit patterns, as integers, which order a NaN above everything. Reading back, a lane
@@ -29,7 +29,6 @@ constexpr int kBlockLanes = 8;                            // lanes of one block
 constexpr int kLaneValues = INDEXER_BLOCK / kBlockLanes;  // values of one lane: 16, in two pieces of 8 columns
 constexpr int kPiece = 8;
 constexpr int kPieces = kLaneValues / kPiece;
-constexpr int kBlocksAhead = 2;                           // blocks that a lane has in flight
 constexpr uint32_t kAmaxFloorBits = (127u - 64u) << 23;   // 2^-64
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -123,121 +122,115 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
   begin_after_prior_grids();
   const int lane = threadIdx.x % kBlockLanes;
   const T* x = static_cast<const T*>(p.x);
-  // a group of lanes takes kBlocksAhead consecutive blocks a round; all groups of a warp run the same number of
-  // rounds (the shuffles name the whole warp)
+  // all groups of lanes of a warp run the same number of rounds (the shuffles name the whole warp)
   constexpr uint32_t kGroups = 32 / kBlockLanes;
   const uint32_t group = (blockIdx.x * kThreads + threadIdx.x) / kBlockLanes;
-  const uint32_t stride = gridDim.x * (kThreads / kBlockLanes) * kBlocksAhead;
-  for (uint32_t u0 = group / kGroups * kGroups * kBlocksAhead; u0 < p.units; u0 += stride) {
-    uint32_t bits[kBlocksAhead][kWords], row[kBlocksAhead], kb[kBlocksAhead];
-    int cols[kBlocksAhead];
+  for (uint32_t u0 = group / kGroups * kGroups; u0 < p.units; u0 += gridDim.x * (kThreads / kBlockLanes)) {
+    uint32_t bits[kWords];
+    const uint32_t u = u0 + group % kGroups;
+    const bool live = u < p.units;
+    const uint32_t row = live ? quotient(p.blocks, u) : 0;
+    const uint32_t kb = live ? u - row * p.blocks.d : 0;
+    const int cols = live ? min(p.dim - static_cast<int>(kb) * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
+    const uint32_t t = quotient(p.heads, row);
+    const T* src = x + t * p.x_ts + (row - t * p.heads.d) * p.x_hs + kb * INDEXER_BLOCK;
 #pragma unroll
-    for (int r = 0; r < kBlocksAhead; ++r) {
-      const uint32_t u = u0 + group % kGroups * kBlocksAhead + r;
-      const bool live = u < p.units;
-      row[r] = live ? quotient(p.blocks, u) : 0;
-      kb[r] = live ? u - row[r] * p.blocks.d : 0;
-      cols[r] = live ? min(p.dim - static_cast<int>(kb[r]) * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
-      const uint32_t t = quotient(p.heads, row[r]);
-      const T* src = x + t * p.x_ts + (row[r] - t * p.heads.d) * p.x_hs + kb[r] * INDEXER_BLOCK;
+    for (int i = 0; i < kWords; ++i) bits[i] = 0;
+    if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) bits[r][i] = 0;
-      if constexpr (VEC) {
+      for (int q = 0; q < kPieces; ++q) {
+        const int c = (q * kBlockLanes + lane) * kPiece;
+        if (c < cols) {
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-          const int c = (q * kBlockLanes + lane) * kPiece;
-          if (c < cols[r]) {
-#pragma unroll
-            for (int i = 0; i < kPieceWords / 4; ++i) {
-              const uint4 a = reinterpret_cast<const uint4*>(src + c)[i];
-              uint32_t* w = &bits[r][q * kPieceWords + 4 * i];
-              w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-            }
+          for (int i = 0; i < kPieceWords / 4; ++i) {
+            const uint4 a = reinterpret_cast<const uint4*>(src + c)[i];
+            uint32_t* w = &bits[q * kPieceWords + 4 * i];
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
           }
         }
-      } else {
-        T v[kLaneValues];
+      }
+    } else {
+      T v[kLaneValues];
 #pragma unroll
-        for (int i = 0; i < kLaneValues; ++i) {
-          const int c = lane + i * kBlockLanes;
-          v[i] = c < cols[r] ? src[c] : from_float<T>(0.0f);
+      for (int i = 0; i < kLaneValues; ++i) {
+        const int c = lane + i * kBlockLanes;
+        v[i] = c < cols ? src[c] : from_float<T>(0.0f);
+      }
+      memcpy(bits, v, sizeof(v));
+    }
+    const uint32_t top = max(block_top<T>(bits), kAmaxFloorBits);
+    if (cols == 0) continue;
+    uint8_t* code;
+    float* scale_at;
+    if constexpr (SLOTS) {
+      const int32_t s = p.slots[row];
+      const uint32_t slot = static_cast<uint32_t>(s);
+      if (slot >= p.capacity) {  // negative ones too
+        if (s != -1 && lane == 0 && kb == 0) atomicAdd(&g_guard_hits, 1u);
+        continue;
+      }
+      const uint32_t page = quotient(p.page_size, slot), off = slot - page * p.page_size.d;
+      code = p.codes + page * p.code_ps + off * p.code_ts + kb * INDEXER_BLOCK;
+      scale_at = p.scales + page * p.scale_ps + off * p.scale_ts + kb;
+    } else {
+      code = p.codes + row * static_cast<int64_t>(p.dim) + kb * INDEXER_BLOCK;
+      scale_at = p.scales + (row * static_cast<int64_t>(p.blocks.d) + kb);
+    }
+
+    T typed[kLaneValues];
+    float v[kLaneValues], scale;
+    memcpy(typed, bits, sizeof(typed));
+#pragma unroll
+    for (int i = 0; i < kLaneValues; ++i) v[i] = to_float(typed[i]);
+    uint32_t c[kLaneValues / 4];  // four codes each
+    if (top >= kInfBits) {
+      scale = __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int i = 0; i < kLaneValues / 4; ++i) c[i] = 0x7f7f7f7fu;
+    } else if (p.pow2) {
+      // amax = m 2^e, 1 <= m < 2: 448 = 1.75 * 2^8, so 2^(e-8) while m <= 1.75, else 2^(e-7)
+      const uint32_t e = (top >> 23) - 8u + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
+      scale = __uint_as_float(e << 23);
+      const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+      for (int i = 0; i < kLaneValues / 4; ++i) c[i] = codes_of(&v[4 * i], inv) | codes_of(&v[4 * i + 2], inv) << 16;
+    } else {
+      scale = over_448(__uint_as_float(top));
+      // the two quotients enclose the real one by 2^-22 or more on each side
+      const float inv = about_inverse(scale), low = inv * (1.0f - 0x1p-21f), high = inv * (1.0f + 0x1p-21f);
+      // Of 16-bit values, x / amax has numerator and denominator below 2^11, a border between codes 2^5: it lies on
+      // the border or 2^-16 of it away. So where the codes differ (by one, then), x * 448 / amax is on the border,
+      // and x / scale is where the rounding of the scale has put it: above, below, or on it (to the even code).
+      const float rest = fmaf(-448.0f, scale, __uint_as_float(top));
+      [[maybe_unused]] const uint32_t up = rest > 0.0f ? 0x01010101u : 0u, even = rest == 0.0f ? 0x01010101u : 0u;
+#pragma unroll
+      for (int i = 0; i < kLaneValues / 4; ++i) {
+        c[i] = codes_of(&v[4 * i], low) | codes_of(&v[4 * i + 2], low) << 16;
+        const uint32_t differ = c[i] ^ (codes_of(&v[4 * i], high) | codes_of(&v[4 * i + 2], high) << 16);
+        if constexpr (sizeof(T) == 2) {
+          c[i] += differ & (up | (c[i] & even));
+        } else if (differ != 0u) {
+          c[i] = e4m3x2(quotient_to_odd(v[4 * i], scale, inv), quotient_to_odd(v[4 * i + 1], scale, inv)) |
+                 e4m3x2(quotient_to_odd(v[4 * i + 2], scale, inv), quotient_to_odd(v[4 * i + 3], scale, inv)) << 16;
         }
-        memcpy(bits[r], v, sizeof(v));
       }
     }
+    if constexpr (VEC) {
 #pragma unroll
-    for (int r = 0; r < kBlocksAhead; ++r) {
-      const uint32_t top = max(block_top<T>(bits[r]), kAmaxFloorBits);
-      if (cols[r] == 0) continue;
-      uint8_t* code;
-      float* scale_at;
-      if constexpr (SLOTS) {
-        const int32_t s = p.slots[row[r]];
-        const uint32_t slot = static_cast<uint32_t>(s);
-        if (slot >= p.capacity) {  // negative ones too
-          if (s != -1 && lane == 0 && kb[r] == 0) atomicAdd(&g_guard_hits, 1u);
-          continue;
-        }
-        const uint32_t page = quotient(p.page_size, slot), off = slot - page * p.page_size.d;
-        code = p.codes + page * p.code_ps + off * p.code_ts + kb[r] * INDEXER_BLOCK;
-        scale_at = p.scales + page * p.scale_ps + off * p.scale_ts + kb[r];
-      } else {
-        code = p.codes + row[r] * static_cast<int64_t>(p.dim) + kb[r] * INDEXER_BLOCK;
-        scale_at = p.scales + (row[r] * static_cast<int64_t>(p.blocks.d) + kb[r]);
+      for (int q = 0; q < kPieces; ++q) {
+        const int col = (q * kBlockLanes + lane) * kPiece;
+        if (col < cols) *reinterpret_cast<uint2*>(code + col) = make_uint2(c[2 * q], c[2 * q + 1]);
       }
-
-      T t[kLaneValues];
-      float v[kLaneValues], scale;
-      memcpy(t, bits[r], sizeof(t));
+    } else {
 #pragma unroll
-      for (int i = 0; i < kLaneValues; ++i) v[i] = to_float(t[i]);
-      uint32_t c[kLaneValues / 4];  // four codes each
-      if (top >= kInfBits) {
-        scale = __uint_as_float(0x7fffffffu);
-#pragma unroll
-        for (int i = 0; i < kLaneValues / 4; ++i) c[i] = 0x7f7f7f7fu;
-      } else if (p.pow2) {
-        // amax = m 2^e, 1 <= m < 2: 448 = 1.75 * 2^8, so 2^(e-8) while m <= 1.75, else 2^(e-7)
-        const uint32_t e = (top >> 23) - 8u + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
-        scale = __uint_as_float(e << 23);
-        const float inv = __uint_as_float((254u - e) << 23);
-#pragma unroll
-        for (int i = 0; i < kLaneValues / 4; ++i) c[i] = codes_of(&v[4 * i], inv) | codes_of(&v[4 * i + 2], inv) << 16;
-      } else {
-        scale = over_448(__uint_as_float(top));
-        // the two quotients enclose the real one by 2^-22 or more on each side
-        const float inv = about_inverse(scale), low = inv * (1.0f - 0x1p-21f), high = inv * (1.0f + 0x1p-21f);
-        uint32_t differ = 0;
-#pragma unroll
-        for (int i = 0; i < kLaneValues / 4; ++i) {
-          c[i] = codes_of(&v[4 * i], low) | codes_of(&v[4 * i + 2], low) << 16;
-          differ |= c[i] ^ (codes_of(&v[4 * i], high) | codes_of(&v[4 * i + 2], high) << 16);
-        }
-        if (differ != 0u) {
-#pragma unroll
-          for (int i = 0; i < kLaneValues / 4; ++i) {
-            c[i] = e4m3x2(quotient_to_odd(v[4 * i], scale, inv), quotient_to_odd(v[4 * i + 1], scale, inv)) |
-                   e4m3x2(quotient_to_odd(v[4 * i + 2], scale, inv), quotient_to_odd(v[4 * i + 3], scale, inv)) << 16;
-          }
-        }
+      for (int i = 0; i < kLaneValues; ++i) {
+        const int col = lane + i * kBlockLanes;
+        if (col < cols) code[col] = static_cast<uint8_t>(c[i / 4] >> (8 * (i & 3)));
       }
-      if constexpr (VEC) {
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-          const int col = (q * kBlockLanes + lane) * kPiece;
-          if (col < cols[r]) *reinterpret_cast<uint2*>(code + col) = make_uint2(c[2 * q], c[2 * q + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLaneValues; ++i) {
-          const int col = lane + i * kBlockLanes;
-          if (col < cols[r]) code[col] = static_cast<uint8_t>(c[i / 4] >> (8 * (i & 3)));
-        }
-      }
-      if (lane == 0) {
-        if constexpr (SLOTS) *scale_at = scale;
-        else *scale_at = p.weights != nullptr ? p.weights[row[r]] * scale : scale;
-      }
+    }
+    if (lane == 0) {
+      if constexpr (SLOTS) *scale_at = scale;
+      else *scale_at = p.weights != nullptr ? p.weights[row] * scale : scale;
     }
   }
 }
@@ -297,7 +290,7 @@ unsigned grid_for(int64_t threads, int64_t most) {
 
 template <typename T>
 cudaError_t launch_quantise(const QuantParams& p, bool vec, int sms, cudaStream_t stream) {
-  constexpr int64_t kWarpUnits = 32 / kBlockLanes * kBlocksAhead;
+  constexpr int64_t kWarpUnits = 32 / kBlockLanes;
   const unsigned grid = grid_for((static_cast<int64_t>(p.units) + kWarpUnits - 1) / kWarpUnits * 32, int64_t(sms) * 8);
   if (p.slots != nullptr)
     return vec ? launch(quantise_kernel<T, true, true>, grid, kThreads, 0, stream, p)

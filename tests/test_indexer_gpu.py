@@ -288,6 +288,30 @@ def test_quantise_at_the_borders_between_codes(fw):
         assert same_quantised(*fw.indexer_quantise(x, scale_format=fmt), quantise_ref(x, fmt))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantise_16_bit_values_on_every_border(fw, dtype):
+    """For every mantissa of the largest value, all values of the type whose quotients come near a border
+    between codes: those on it depend on the rounding of the scale alone."""
+    bits = 8 if dtype is torch.bfloat16 else 11
+    g = grid()
+    mid = (g[1:] + g[:-1]) / 2
+    rows = []
+    for a in range(2 ** (bits - 1), 2 ** bits):
+        top = float(a)
+        at = torch.from_numpy(mid * top / 448.0).to(dtype).double()
+        step = torch.exp2(torch.floor(torch.log2(at.clamp(min=2.0 ** -24))) - (bits - 1))
+        v = torch.cat([at, at + step, at - step]).clamp(0.0, top)
+        v[1::2] *= -1
+        for i in range(0, len(v), 127):
+            part = torch.zeros(128, dtype=torch.float64)
+            part[:len(v[i:i + 127])] = v[i:i + 127]
+            part[127] = top
+            rows.append(part)
+    x = torch.stack(rows).to(dtype).cuda()
+    for fmt in ("fp32", "pow2"):
+        assert same_quantised(*fw.indexer_quantise(x, scale_format=fmt), quantise_ref(x, fmt))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_quantise_extremes_and_what_is_not_finite(fw, dtype):
     big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal
