@@ -213,28 +213,17 @@ cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half
   p.pairs = divisor(pairs);
   p.turn_items = divisor(turn_items);
   p.copy_items = copy_items > 0 ? divisor(copy_items) : Divisor{0, 0, 0};
-  // a launch has fewer than 2^31 CTAs: a longer call is cut into launches of so many tokens
-  if (head_tiles * segments > INT64_C(1) << 30) return cudaErrorInvalidValue;
-  const int64_t step = (INT64_C(1) << 30) / (head_tiles * segments) * tile_tokens;
-  for (int64_t t = 0; t < tokens; t += step) {
-    const int64_t n = tokens - t < step ? tokens - t : step;
-    p.tokens = static_cast<int32_t>(n);
-    const unsigned grid = static_cast<unsigned>((n + tile_tokens - 1) / tile_tokens * head_tiles * segments);
-    cudaError_t e;
-    if (v == 2 * kV)
-      e = launch(rotary_kernel<T, 2 * kV, false>, grid, kThreads, 0, stream, p);
-    else if (v == kV)
-      e = half ? launch(rotary_kernel<T, kV, true>, grid, kThreads, 0, stream, p)
-               : launch(rotary_kernel<T, kV, false>, grid, kThreads, 0, stream, p);
-    else
-      e = half ? launch(rotary_kernel<T, 1, true>, grid, kThreads, 0, stream, p)
-               : launch(rotary_kernel<T, 1, false>, grid, kThreads, 0, stream, p);
-    if (e != cudaSuccess) return e;
-    p.x = static_cast<const T*>(p.x) + n * p.x_ts;
-    p.out = static_cast<T*>(p.out) + n * p.out_ts;
-    p.positions += n;
-  }
-  return cudaSuccess;
+  p.tokens = static_cast<int32_t>(tokens);
+  // more CTAs than a launch takes would need an output of more than the device's memory
+  const int64_t blocks = (tokens + tile_tokens - 1) / tile_tokens * head_tiles * segments;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (v == 2 * kV) return launch(rotary_kernel<T, 2 * kV, false>, grid, kThreads, 0, stream, p);
+  if (v == kV)
+    return half ? launch(rotary_kernel<T, kV, true>, grid, kThreads, 0, stream, p)
+                : launch(rotary_kernel<T, kV, false>, grid, kThreads, 0, stream, p);
+  return half ? launch(rotary_kernel<T, 1, true>, grid, kThreads, 0, stream, p)
+              : launch(rotary_kernel<T, 1, false>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace
