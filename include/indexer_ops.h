@@ -79,8 +79,8 @@ size_t indexer_cache_bytes(void);
 /* Rotary positions. x, out: [tokens, heads, dim] of `dtype`, unit column stride, token
  * and head strides in elements (out's rows must not overlap; out may be x itself, with
  * the same strides, and must otherwise not overlap it; x's strides may be 0).
- * positions [tokens] int32 (any sign), freqs [rot_dim / 2] fp64, in radians per
- * position. With angle = positions[t] * freqs[i], c = scale * cos(angle),
+ * positions [tokens] int32 (any sign), freqs [rot_dim / 2] fp64, finite, in radians
+ * per position. With angle = positions[t] * freqs[i], c = scale * cos(angle),
  * s = scale * sin(angle), pair i = (a, b) becomes
  *   (a c - b s, b c + a s)   or, with transpose != 0, the gradient's (a c + b s, b c - a s),
  * computed in fp32 and rounded once. Columns outside [start, start + rot_dim) are copied.

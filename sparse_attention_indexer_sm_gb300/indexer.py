@@ -98,11 +98,12 @@ def _choice(value, table, name: str) -> int:
     return table[value]
 
 
-def _on(stream, call, given, *args):
-    """A call on a stream of the caller's: outputs made by it are in use there until its kernel has ended."""
+def _on(stream, call, *args):
+    """A call on a stream of the caller's. Its tensors, given or made by it, are in use there until its kernel has
+    ended: none of their memory is handed out again before that."""
     out = call(*args, stream.cuda_stream)
-    for t, g in zip(out if isinstance(out, tuple) else (out,), given):
-        if g is None:
+    for t in (*args, *(out if isinstance(out, tuple) else (out,))):
+        if isinstance(t, torch.Tensor):
             t.record_stream(stream)
     return out
 
@@ -158,7 +159,7 @@ def indexer_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor
     f = (_binding or _load_binding()).rotary
     how = _choice(layout, _LAYOUTS, "layout")
     if stream is not None:
-        return _on(stream, f, (out,), x, positions, freqs, how, start, scale, transpose, out)
+        return _on(stream, f, x, positions, freqs, how, start, scale, transpose, out)
     return f(x, positions, freqs, how, start, scale, transpose, out, None)
 
 
@@ -177,7 +178,7 @@ def indexer_quantise(x: torch.Tensor, *, scale_format: str = "fp32",
     f = (_binding or _load_binding()).quantise
     fmt = _choice(scale_format, _FORMATS, "scale_format")
     if stream is not None:
-        return _on(stream, f, (codes, scales), x, fmt, weights, codes, scales)
+        return _on(stream, f, x, fmt, weights, codes, scales)
     return f(x, fmt, weights, codes, scales, None)
 
 
@@ -190,7 +191,10 @@ def indexer_cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tenso
     either, and counted (indexer_guard_hits). Slots should differ from each other."""
     f = (_binding or _load_binding()).cache_write
     fmt = _choice(scale_format, _FORMATS, "scale_format")
-    f(x, slots, codes, scales, fmt, None if stream is None else stream.cuda_stream)
+    if stream is not None:
+        _on(stream, f, x, slots, codes, scales, fmt)
+    else:
+        f(x, slots, codes, scales, fmt, None)
 
 
 def indexer_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, *,
@@ -202,7 +206,7 @@ def indexer_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.T
     f = (_binding or _load_binding()).cache_read
     kind = _choice(dtype, _DTYPES, "dtype")
     if stream is not None:
-        return _on(stream, f, (out,), codes, scales, slots, kind, out)
+        return _on(stream, f, codes, scales, slots, kind, out)
     return f(codes, scales, slots, kind, out, None)
 
 
@@ -224,7 +228,7 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, 
     outside the cache get -inf and are counted (indexer_guard_hits)."""
     f = (_binding or _load_binding()).scores
     if stream is not None:
-        return _on(stream, f, (out,), q, weights, codes, scales, page_table, seq_lens, row_len, out)
+        return _on(stream, f, q, weights, codes, scales, page_table, seq_lens, row_len, out)
     return f(q, weights, codes, scales, page_table, seq_lens, row_len, out, None)
 
 

@@ -738,3 +738,59 @@ def test_captured_backward(fw):
         torch.cuda.synchronize()
         check(y, *rotary_ref(x.detach(), positions, freqs, "half", 0, 1.0, False))
         check(grad, *rotary_ref(dy, positions, freqs, "half", 0, 1.0, True))
+
+
+def test_example_decodes(fw):
+    """examples/indexer_decode.py: its last step's scores, selection and rows."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "indexer_decode.py")
+    spec = importlib.util.spec_from_file_location("indexer_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.main(["--batch", "3", "--context", "300", "--k", "50", "--steps", "4"])
+    ix = got["indexer"]
+    assert ix.lens.tolist() == [300] * 3
+    q = fw.indexer_rotary(ix.q, ix.lens - 1, ix.freqs, start=64, scale=ix.scale)
+    q8, w = fw.indexer_quantise(q, weights=ix.weights)
+    check_scores(got["scores"], q8[:, None], w[:, None], ix.codes, ix.scales, ix.page_table, ix.lens[:, None], 300)
+    slot = ix.page_table.long()[:, torch.arange(300).cuda() // 64] * 64 + torch.arange(300).cuda() % 64
+    want = slot.gather(1, got["scores"].topk(50, 1).indices)
+    assert torch.equal(got["picked"].long().sort(1).values, want.sort(1).values)
+    assert torch.equal(got["rows"], fw.indexer_cache_read(ix.codes, ix.scales, got["picked"]))
+
+
+def test_calls_of_more_parts_than_one_launch_numbers(fw):
+    """More than 2**30 rows: they are cut into launches, which have to fit together."""
+    heads, tokens = 16384, 66000
+    row = torch.randn((1, heads, 1), generator=gen(3)).to(torch.bfloat16).cuda()
+    codes, scales = fw.indexer_quantise(row.expand(tokens, heads, 1))
+    one = fw.indexer_quantise(row)
+    assert same_quantised(*one, quantise_ref(row, "fp32"))
+    for t in range(0, tokens, 4000):  # a piece at a time: comparisons make copies
+        part = slice(t, t + 4000)
+        assert bool((codes[part].view(torch.uint8) == one[0].view(torch.uint8)).all())
+        assert bool((scales[part] == one[1]).all())
+    del codes, scales
+    cache = torch.randint(0, 120, (64, 16, 16), generator=gen(4), dtype=torch.uint8).cuda().view(E4M3)
+    factors = torch.rand((64, 16, 1), generator=gen(5)).cuda()
+    slots = torch.arange(1024, dtype=torch.int32).cuda()
+    want = fw.indexer_cache_read(cache, factors, slots, dtype=torch.bfloat16)
+    got = fw.indexer_cache_read(cache, factors, slots.repeat((1 << 20) + 3), dtype=torch.bfloat16)
+    got = got.view(-1, 1024, 16)
+    for r in range(0, got.shape[0], 1 << 17):
+        assert bool((got[r:r + (1 << 17)] == want).all())
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_scores_of_drawn_shapes(fw, seed):
+    """Shapes from the whole range, ragged, with pages of every kind."""
+    import random
+    rng = random.Random(seed)
+    b, n, h = rng.randint(1, 40), rng.choice([1, 1, 2, 3, 5, 8, 40]), rng.choice([1, 8, 15, 16, 31, 48, 64, 65, 128])
+    row_len, size = rng.randint(1, 5000), rng.choice([1, 2, 3, 12, 16, 48, 64, 128, 192, 256])
+    args = scores_inputs(seed + 100, b, n, h, row_len, size, layout=rng.choice(["apart", "row"]))
+    got = fw.indexer_scores(*args)
+    q, w, codes, scales, table, lens, _ = args
+    for i in {0, b // 2, b - 1}:
+        check_scores(got[i * n:(i + 1) * n], q[i:i + 1], w[i:i + 1], codes, scales, table[i:i + 1], lens[i:i + 1], row_len)
