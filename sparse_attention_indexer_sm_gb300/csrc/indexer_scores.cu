@@ -11,15 +11,21 @@
 // operations and is bound by memory; a prompt's chunk shares a key tile between the queries of a group
 // and is bound by the relu-sum of the epilogue and by the tensor cores, about evenly.
 //
-// One CTA an SM, persistent over (sequence, query group, chunk of tiles). A tile's products are one unit of up
-// to 128 columns, or two (the same number for a whole launch). Its warps share out the work; a lone warp takes some 50 cycles for each barrier it
-// looks at, so that every role that a tile passes through has two warps or four, which take turns:
-//   warps 0, 1  page ids and TMA copies: a ring of key tiles, two buffers of queries
-//   warps 2, 3  tcgen05.mma, each for the units of one epilogue group
-//   warps 4-7   the keys' scales, two tiles at once: they are a dependent load behind the page id,
-//               which no warp with other work should wait for
-//   warps 8-11, 12-15  two epilogue groups that take the units in turn, each with a weight for every column
-//               in registers: from shared memory a weight costs as much as four columns' arithmetic
+// One CTA an SM, persistent over (sequence, query group, chunk of tiles). A tile's products are one unit of columns, or
+// two (the same number for a whole launch). The warps of a CTA share out the work:
+//   loaders      page ids and TMA copies: a ring of key tiles, two buffers of queries
+//   multipliers  tcgen05.mma
+//   scalers      the keys' scales, two tiles at once: they are a dependent load behind the page id,
+//                which no warp with other work should wait for
+//   epilogue     groups of four warps, each with a weight for every one of its columns in registers: from
+//                shared memory a weight costs as much as four columns' arithmetic
+// in one of two plans. A lone warp takes some 50 cycles for each barrier that it looks at, so with up to 128 columns, where
+// a tile is soon done, every role that a tile passes through has two warps or four that take turns. With more
+// columns an epilogue group's work on a tile outlasts that, and what counts is how many warps hide each other's latencies: four
+// groups, of a quarter of the columns each (2048 queries over 32768 keys, 16 and 64 heads: 170 and 588 us against
+// 192 and 617 with two groups). There the epilogue still bounds the kernel, at 63% of the issue slots and 60% of the
+// integer pipe (relu is one of its instructions); the tensor pipe is at 37%. Moving half of the relus to the fp32 pipe (a
+// saturating product) changed nothing, nor did larger or fewer loads from TMEM: what is left is latency.
 // A barrier's parity tells a phase from the next one, but not from the one after that. So each place of a
 // ring belongs to the same warp of a role throughout: tiles and units are dealt out by their running
 // numbers over the whole launch, and the rings' lengths are multiples of the numbers of warps.
@@ -38,23 +44,30 @@ namespace {
 
 constexpr int kDim = INDEXER_SCORE_DIM;  // bytes of a key's codes: one swizzled row
 constexpr int kTile = 128;               // keys of a tile: the rows of one MMA, the lanes of TMEM
-constexpr int kThreads = 512;
-constexpr int kLoaders = 2, kScalers = 4;  // warps (and two for the MMAs)
-constexpr int kEpilogue = 8;               // first warp of the epilogue
 constexpr int kMaxColumns = 256;         // heads of a group's queries
-constexpr int kWarpColumns = 128;        // columns of a unit, N of its MMAs: a register each in the epilogue
-// Registers of a thread: 128 at launch, moved from the first eight warps to the epilogue
-// (512 * 128 = 256 * 64 + 256 * 192).
-constexpr int kFewRegisters = 64, kManyRegisters = 192;
+// How a CTA's warps share out its work, by the number of epilogue groups. Registers of a thread: what a launch of so many
+// threads has of 65536, moved from the first warps to the epilogue (512 * 128 = 256 * 64 + 256 * 192, and
+// 640 * 96 = 128 * 64 + 512 * 104).
+template <int kGroups> struct Plan;
+template <> struct Plan<2> {  // the groups take units in turn
+  static constexpr int kLoaders = 2, kMultipliers = 2, kScalers = 4, kFewRegisters = 64, kManyRegisters = 192;
+  static constexpr int kColumns = 128;  // of a unit, N of its MMAs: a register each in the epilogue
+};
+template <> struct Plan<4> {  // each group takes a quarter of the columns of every tile
+  static constexpr int kLoaders = 1, kMultipliers = 1, kScalers = 2, kFewRegisters = 64, kManyRegisters = 104;
+  static constexpr int kColumns = 64;
+};
+template <int kGroups> constexpr int kFirstWarp = Plan<kGroups>::kLoaders + Plan<kGroups>::kMultipliers + Plan<kGroups>::kScalers;
+template <int kGroups> constexpr int kThreads = 32 * (kFirstWarp<kGroups> + 4 * kGroups);
+
 constexpr int kTmemColumns = 512;
 constexpr int kKeyStages = 8;
 constexpr int kMaxTmemStages = 8;
 constexpr int kScaleBatch = 2;
-static_assert(kKeyStages % kLoaders == 0 && kKeyStages % 2 == 0 && 4 % kScalers == 0 && kMaxTmemStages == 8, "a ring's place belongs to one warp of a role");
 constexpr int kMaxChunk = 64;            // tiles of an item
 constexpr int kItemCost = 4;             // tiles that the start of an item costs
 constexpr int kMaxGroup = 16;            // queries of a group
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;       // at most
 constexpr int kWaitLimit = 1 << 17;      // tries of a wait before it is given up,
 constexpr uint32_t kWaitNs = 20000;      // each of which may sleep this long: 2.6 s in all
 
@@ -86,7 +99,7 @@ struct Shared {
   alignas(1024) uint8_t keys[kKeyStages][kTile * kDim];
   alignas(1024) uint8_t queries[2][kMaxColumns * kDim];
   alignas(16) float scales[kMaxTmemStages][kTile];
-  alignas(16) float weights[kEpilogueWarps][kWarpColumns];  // each warp's own copy: no barrier among them
+  alignas(16) float weights[1024];  // a copy for each epilogue warp of its columns': no barrier among them
   int32_t lens[kEpilogueWarps][kMaxGroup];
   alignas(8) uint64_t key_full[kKeyStages], key_empty[kKeyStages];
   uint64_t query_full[2], query_empty[2];
@@ -316,9 +329,11 @@ __device__ __forceinline__ void item_ready(const ScoresParams& p, Item& it) {
 
 // The copies of every kLoaders-th tile. kPieces: copies of a tile that a lane may have to issue; or the page
 // ids of its one copy, where kGather says that a page is one row.
-template <int kPieces, bool kGather>
+template <int kGroups, int kPieces, bool kGather>
 __device__ __forceinline__ void load_keys(const ScoresParams& p, Shared& s, const CUtensorMap* key_map,
                                           const CUtensorMap* query_map, int head_rows, int turn) {
+  constexpr int kLoaders = Plan<kGroups>::kLoaders;
+  static_assert(kKeyStages % kLoaders == 0, "a ring's place belongs to one warp");
   const int lane = threadIdx.x & 31;
   const int pieces = kTile / p.piece_rows;
   const uint32_t piece_bytes = static_cast<uint32_t>(p.piece_rows) * kDim;
@@ -399,16 +414,22 @@ __device__ __forceinline__ void load_keys(const ScoresParams& p, Shared& s, cons
     for (uint32_t n = items; n < items + 2; ++n) bar_drain(&s.query_full[n & 1], (n >> 1 & 1u) ^ 1u);
 }
 
-// A warp's tiles of an item, where those of epilogue group `wg` are every one (two units a tile) or every second one
-// of the launch (one unit a tile).
+// The first tile of an item that is epilogue group `wg`'s, and the step to its next: with two groups every tile (two
+// units a tile) or every second one of the launch (one unit a tile), with four every tile.
+template <int kGroups>
 __device__ __forceinline__ int first_tile(const ScoresParams& p, const Item& it, int wg, uint32_t tiles) {
-  return it.first + (p.units == 1 ? static_cast<int>((wg ^ tiles) & 1u) : 0);
+  return it.first + (kGroups == 2 && p.units == 1 ? static_cast<int>((wg ^ tiles) & 1u) : 0);
 }
+template <int kGroups>
+__device__ __forceinline__ int tile_step(const ScoresParams& p) { return kGroups == 2 ? 3 - p.units : 1; }
 
-// The products of the units of epilogue group `wg`.
+// The products of the units of epilogue group `wg` of two; of four groups, of all of them.
+template <int kGroups>
 __device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint32_t tmem, int head_rows, int wg) {
-  const uint32_t half = (1u << p.tmem_shift) / 2;  // the group's TMEM stages: wg, wg + 2, ...
-  uint32_t tiles = 0, items = 0, units = 0;        // so far; units: of this group
+  // the TMEM stages of this warp's units: of two, wg, wg + 2, ...
+  constexpr uint32_t kStep = Plan<kGroups>::kMultipliers;
+  const uint32_t stages = (1u << p.tmem_shift) / kStep, stage_shift = p.tmem_shift - (kStep - 1);
+  uint32_t tiles = 0, items = 0, units = 0;  // so far; units: of this warp
   bool ok = true;
   Item next_item = item_at(p, blockIdx.x);
   for (int64_t i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
@@ -421,10 +442,10 @@ __device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint3
     const int queries_here = min(it.count - u * p.unit_queries, p.unit_queries);  // none in the rest of a short group
     // fp32 accumulators, e4m3 operands, both K-major, M = 128
     const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(queries_here * head_rows) >> 3) << 17) | ((kTile >> 4) << 24);
-    const uint32_t b = matrix_desc(smem_addr(s.queries[items & 1])) + u * (kWarpColumns * kDim / 16);
-    for (int t = first_tile(p, it, wg, tiles); ok && t < it.seen; t += 3 - p.units, ++units) {
+    const uint32_t b = matrix_desc(smem_addr(s.queries[items & 1])) + u * (Plan<kGroups>::kColumns * kDim / 16);
+    for (int t = first_tile<kGroups>(p, it, wg, tiles); ok && t < it.seen; t += tile_step<kGroups>(p), ++units) {
       const uint32_t n = tiles + (t - it.first), key = n % kKeyStages;
-      const uint32_t stage = wg + 2 * (units & (half - 1)), phase = (units >> (p.tmem_shift - 1)) & 1u;
+      const uint32_t stage = wg + kStep * (units & (stages - 1)), phase = (units >> stage_shift) & 1u;
       // both barriers at once while neither has to be waited for
       const bool keys_here = bar_try(smem_addr(&s.key_full[key]), n / kKeyStages & 1u);
       const bool stage_free = bar_try(smem_addr(&s.tmem_empty[stage]), phase ^ 1u);
@@ -437,7 +458,7 @@ __device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint3
         if (queries_here > 0) mma_tile(tmem + stage * p.tmem_stride, a, b, idesc);
         mma_commit(&s.tmem_full[stage]);
         mma_commit(&s.key_empty[key]);
-        if (p.units == 1) bar_arrive(&s.key_empty[key]);  // for the other warp, which has no unit here
+        if (kStep == 2 && p.units == 1) bar_arrive(&s.key_empty[key]);  // for the other warp, which has no unit here
       }
       __syncwarp();
     }
@@ -456,8 +477,9 @@ __device__ __forceinline__ void multiply(const ScoresParams& p, Shared& s, uint3
 // scales, so that each latency is met once in a batch. They go where their unit's products go, to a
 // place for each TMEM stage, and share its barriers. A lane brings four neighbouring keys;
 // kQuads: they lie on one page.
-template <bool kQuads>
+template <int kGroups, bool kQuads>
 __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, int turn) {
+  constexpr int kScalers = Plan<kGroups>::kScalers;
   constexpr int kPages = kQuads ? 1 : 4;
   const int lane = threadIdx.x & 31;
   const int step = kScalers / p.units;                  // tiles from one unit of this warp to its next
@@ -543,10 +565,11 @@ struct Lane {
   bool no_page;          // this key is on none
 };
 
-// Columns from C * kLoad on, which are on their way to r: the next load is sent off before they are summed.
+// Columns from C * kLoad on, which are on their way to r. With registers for it (two epilogue groups) the next load is
+// sent off before they are summed: 64 or 128 heads 4% faster; of four groups, whose warps hide it from one another, after.
 // Whether the next unit is there already: asked before the last sums, for use after them.
-template <int kHeads, int kLoad, bool kWhole, int C>
-__device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kWarpColumns], float (&r)[kLoad],
+template <int kHeads, int kLoad, bool kWhole, int C, int kColumns>
+__device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kColumns], float (&r)[kLoad],
                                              uint64_t acc0, uint64_t acc1) {
   tmem_wait<kLoad>(r);
   auto add = [&]() {
@@ -571,11 +594,12 @@ __device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kWa
       acc0 = acc1 = 0;
     }
   };
-  if constexpr ((C + 1) * kLoad < kWarpColumns) {
+  if constexpr ((C + 1) * kLoad < kColumns) {
     if ((C + 1) * kLoad < l.columns) {
       float next[kLoad];
+      if constexpr (kColumns == 64) add();
       tmem_load<kLoad>(l.tmem + (C + 1) * kLoad, next);
-      add();
+      if constexpr (kColumns != 64) add();
       return columns_from<kHeads, kLoad, kWhole, C + 1>(l, w, next, acc0, acc1);
     }
   }
@@ -588,16 +612,18 @@ __device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kWa
   return ready;
 }
 
-// One epilogue warp: relu, weights and the sum over heads of its 32 lanes (keys), for every second unit.
+// One epilogue warp: relu, weights and the sum over heads of its 32 lanes (keys), for its group's units or columns.
 // kHeads: columns of a query.
-template <int kHeads>
+template <int kGroups, int kHeads>
 __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_t tmem, int wg) {
   constexpr int kLoad = 16;                         // columns of a load
-  constexpr int kQueries = kWarpColumns / kHeads;   // queries of a unit at most
-  constexpr int kBring = kWarpColumns / 32;         // weights that a lane brings
-  const int tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x / 32 - kEpilogue;
+  constexpr int kColumns = Plan<kGroups>::kColumns;
+  constexpr int kQueries = kColumns / kHeads;       // queries of a group's columns at most
+  constexpr int kBring = kColumns / 32;             // weights that a lane brings
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x / 32 - kFirstWarp<kGroups>;
+  float* const weights = s.weights + warp * kColumns;
   const float minus_inf = __int_as_float(0xff800000);
-  const int first = p.units == 2 ? wg * kQueries : 0;  // of this warp's queries in a group
+  const int first = kGroups == 4 || p.units == 2 ? wg * kQueries : 0;  // of this warp's queries in a group of queries
   float bring[kBring];
   auto weights_of = [&](const Item& it) {
     const float* src = p.weights + (it.query + first) * p.heads;
@@ -609,10 +635,12 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
   };
   Lane l;
   l.row_len = p.row_len;
-  const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(tid & ~31) << 16);
-  const uint32_t stages = 1u << p.tmem_shift;      // the group's own: wg, wg + 2, ...
+  const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(tid & ~31) << 16) + (kGroups == 4 ? wg * kColumns : 0);
+  // the group's TMEM stages: of two groups wg, wg + 2, ..., of four all of them
+  constexpr uint32_t kStep = kGroups == 2 ? 2 : 1;
+  const uint32_t stages = 1u << p.tmem_shift, first_stage = kGroups == 2 ? wg : 0;
   const uint32_t full_base = smem_addr(s.tmem_full), empty_base = smem_addr(s.tmem_empty);
-  uint32_t tiles = 0, stage = wg, phase = 0;
+  uint32_t tiles = 0, stage = first_stage, phase = 0;
   bool ready = false;
   Item next_item = item_at(p, blockIdx.x);
   weights_of(next_item);
@@ -621,13 +649,13 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     item_ready(p, it);
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kBring; ++k) s.weights[warp][lane + 32 * k] = bring[k];
+    for (int k = 0; k < kBring; ++k) weights[lane + 32 * k] = bring[k];
     if (lane < it.count) s.lens[warp][lane] = it.len;
     __syncwarp();
-    float w[kWarpColumns];
+    float w[kColumns];
 #pragma unroll
-    for (int k = 0; k < kWarpColumns / 4; ++k) {
-      const float4 f = reinterpret_cast<const float4*>(s.weights[warp])[k];
+    for (int k = 0; k < kColumns / 4; ++k) {
+      const float4 f = reinterpret_cast<const float4*>(weights)[k];
       w[4 * k] = f.x, w[4 * k + 1] = f.y, w[4 * k + 2] = f.z, w[4 * k + 3] = f.w;
     }
     const int count = min(max(it.count - first, 0), kQueries);
@@ -636,15 +664,15 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     float* const out = p.out + (it.query + first) * p.row_len;
     next_item = item_at(p, i + gridDim.x);
     weights_of(next_item);  // on their way while this item is worked on
-    const int step = 3 - p.units;
-    for (int t = first_tile(p, it, wg, tiles); t < it.seen; t += step) {
+    const int step = tile_step<kGroups>(p);
+    for (int t = first_tile<kGroups>(p, it, wg, tiles); t < it.seen; t += step) {
       const uint32_t at = stage, full = full_base + 8 * stage;
       l.tmem_empty = empty_base + 8 * stage;
       if (!ready) bar_pass(s, full, phase);
       tmem_fence_after();
-      stage += 2;
+      stage += kStep;
       if (stage >= stages) {
-        stage = wg;
+        stage = first_stage;
         phase ^= 1u;
       }
       ready = false;
@@ -668,7 +696,8 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     }
     tiles += it.seen - it.first;
     // tiles that no query of the group sees
-    for (int t = it.seen + (p.units == 2 ? 0 : wg); t < it.end; t += p.units == 2 ? 1 : 2) {
+    const bool in_turn = kGroups == 2 && p.units == 1;
+    for (int t = it.seen + (in_turn ? wg : 0); t < it.end; t += in_turn ? 2 : 1) {
       const int64_t j = static_cast<int64_t>(t) * kTile + tid;
       if (j < p.row_len)
         for (int g = 0; g < count; ++g) out[g * p.row_len + j] = minus_inf;
@@ -687,27 +716,28 @@ __device__ __forceinline__ void fewer_registers() {
 
 // kHeads: heads rounded up to 16, 32, 64 or 128. The rounding's rows of B are zeros (beyond the
 // tensor map's heads) and their weights are 0.
-template <int kHeads>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kGroups, int kHeads>
+__global__ void __launch_bounds__(kThreads<kGroups>, 1)
     scores_kernel(const ScoresParams p, const __grid_constant__ CUtensorMap key_map,
                   const __grid_constant__ CUtensorMap query_map) {
+  using P = Plan<kGroups>;
   extern __shared__ uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKeyStages; ++i) {
       bar_init(&s.key_full[i], 1);
-      bar_init(&s.key_empty[i], 2);
+      bar_init(&s.key_empty[i], P::kMultipliers);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&s.query_full[i], 1);
-      bar_init(&s.query_empty[i], 2);
+      bar_init(&s.query_empty[i], P::kMultipliers);
     }
     for (int i = 0; i < kMaxTmemStages; ++i) {
       bar_init(&s.tmem_full[i], 2);  // the products and the scales
-      bar_init(&s.tmem_empty[i], 4);
+      bar_init(&s.tmem_empty[i], kGroups == 2 ? 4 : 16);  // the warps that read it
     }
-    bar_init(&s.drained, 2);
+    bar_init(&s.drained, P::kMultipliers);
     s.aborted = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -724,17 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   begin_after_prior_grids();
 
-  if (warp < kEpilogue) {
-    fewer_registers<kFewRegisters>();
-    if (warp < kLoaders && p.page_size == 1) load_keys<4, true>(p, s, &key_map, &query_map, kHeads, warp);
-    else if (warp < kLoaders && p.piece_rows >= 4) load_keys<1, false>(p, s, &key_map, &query_map, kHeads, warp);
-    else if (warp < kLoaders) load_keys<4, false>(p, s, &key_map, &query_map, kHeads, warp);
-    else if (warp < kLoaders + 2) multiply(p, s, tmem, kHeads, warp - kLoaders);
-    else if (p.quads != 0) load_scales<true>(p, s, warp - kLoaders - 2);
-    else load_scales<false>(p, s, warp - kLoaders - 2);
+  if (warp < kFirstWarp<kGroups>) {
+    fewer_registers<P::kFewRegisters>();
+    if (warp < P::kLoaders && p.page_size == 1)
+      load_keys<kGroups, 4, true>(p, s, &key_map, &query_map, kHeads, warp);
+    else if (warp < P::kLoaders && p.piece_rows >= 4)
+      load_keys<kGroups, 1, false>(p, s, &key_map, &query_map, kHeads, warp);
+    else if (warp < P::kLoaders)
+      load_keys<kGroups, 4, false>(p, s, &key_map, &query_map, kHeads, warp);
+    else if (warp < P::kLoaders + P::kMultipliers)
+      multiply<kGroups>(p, s, tmem, kHeads, warp - P::kLoaders);
+    else if (p.quads != 0)
+      load_scales<kGroups, true>(p, s, warp - P::kLoaders - P::kMultipliers);
+    else
+      load_scales<kGroups, false>(p, s, warp - P::kLoaders - P::kMultipliers);
   } else {
-    more_registers<kManyRegisters>();
-    reduce<kHeads>(p, s, tmem, (warp - kEpilogue) / 4);
+    more_registers<P::kManyRegisters>();
+    reduce<kGroups, kHeads>(p, s, tmem, (warp - kFirstWarp<kGroups>) / 4);
   }
 
   tmem_fence_before();
@@ -777,7 +813,7 @@ cudaError_t row_map(EncodeTiled encode, CUtensorMap* map, int axes, const uint8_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int kHeads>
+template <int kGroups, int kHeads>
 cudaError_t launch_scores(ScoresParams p, const CUtensorMap& key_map, const CUtensorMap& query_map, unsigned grid,
                           cudaStream_t stream) {
   // set once for each device and kernel: the attribute belongs to the function on that device
@@ -786,12 +822,12 @@ cudaError_t launch_scores(ScoresParams p, const CUtensorMap& key_map, const CUte
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || (prepared.load(std::memory_order_acquire) >> dev & 1u) == 0) {
-    e = cudaFuncSetAttribute(scores_kernel<kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(scores_kernel<kGroups, kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
     if (dev <= 63) prepared.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
-  return launch(scores_kernel<kHeads>, grid, kThreads, kSmemBytes, stream, p, key_map, query_map);
+  return launch(scores_kernel<kGroups, kHeads>, grid, kThreads<kGroups>, kSmemBytes, stream, p, key_map, query_map);
 }
 
 }  // namespace
@@ -859,12 +895,16 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   p.group = kMaxColumns / head_rows < queries ? kMaxColumns / head_rows : queries;
   p.groups = (queries + p.group - 1) / p.group;
   p.tiles = static_cast<int32_t>((row_len + kTile - 1) / kTile);
-  p.unit_queries = kWarpColumns / head_rows;
+  // Groups of queries of more than 128 columns, in columns of 16, 32 or 64 a query: four epilogue groups, a quarter of a
+  // tile's columns each, and one unit a tile; otherwise two, and units of up to 128 columns.
+  const int columns = p.group * head_rows;
+  const int epilogues = columns > 128 && head_rows <= 64 ? 4 : 2;
+  p.unit_queries = epilogues == 4 ? p.group : Plan<2>::kColumns / head_rows;
   p.units = p.group > p.unit_queries ? 2 : 1;
-  // TMEM stages of 32 columns or a larger power of two: 4 or 8 of them
+  // TMEM stages of 32 columns or a larger power of two: 2 of 256, or 4 or 8
   p.tmem_stride = 32;
-  while (p.tmem_stride < kWarpColumns && p.tmem_stride < p.group * head_rows) p.tmem_stride *= 2;
-  p.tmem_shift = p.tmem_stride == kWarpColumns ? 2 : 3;
+  while (p.tmem_stride < columns / p.units) p.tmem_stride *= 2;
+  p.tmem_shift = p.tmem_stride == 256 ? 1 : p.tmem_stride == 128 ? 2 : 3;
   // Tiles of an item: what takes the SM with the most items the least time when every row is full, an
   // item's start counted as kItemCost tiles.
   p.slices = static_cast<int64_t>(batch) * p.groups;
@@ -885,9 +925,15 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
                 static_cast<int64_t>(heads) * kDim, head_rows, p.group);
   if (e != cudaSuccess) return status_of(e);
   const unsigned grid = static_cast<unsigned>(p.items < sms ? p.items : sms);
-  if (head_rows == 16) e = launch_scores<16>(p, key_map, query_map, grid, stream);
-  else if (head_rows == 32) e = launch_scores<32>(p, key_map, query_map, grid, stream);
-  else if (head_rows == 64) e = launch_scores<64>(p, key_map, query_map, grid, stream);
-  else e = launch_scores<128>(p, key_map, query_map, grid, stream);
+  if (epilogues == 4) {
+    if (head_rows == 16) e = launch_scores<4, 16>(p, key_map, query_map, grid, stream);
+    else if (head_rows == 32) e = launch_scores<4, 32>(p, key_map, query_map, grid, stream);
+    else e = launch_scores<4, 64>(p, key_map, query_map, grid, stream);
+  } else {
+    if (head_rows == 16) e = launch_scores<2, 16>(p, key_map, query_map, grid, stream);
+    else if (head_rows == 32) e = launch_scores<2, 32>(p, key_map, query_map, grid, stream);
+    else if (head_rows == 64) e = launch_scores<2, 64>(p, key_map, query_map, grid, stream);
+    else e = launch_scores<2, 128>(p, key_map, query_map, grid, stream);
+  }
   return status_of(e);
 }
