@@ -4,6 +4,7 @@
 // back to torch. Errors: TypeError and ValueError for arguments, the package's TopkError for a status.
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
@@ -104,7 +105,8 @@ cudaStream_t stream_of(const Stream& stream, const Tensor& x) {
 }
 
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& x) {
-  return at::empty(shape, x.options().dtype(type).requires_grad(false));
+  // straight from the caching allocator: at::empty's way through the dispatcher takes longer than the checks
+  return at::detail::empty_cuda(shape, type, x.device(), std::nullopt);
 }
 
 // ---------------------------------------------------------------- rotary positions
