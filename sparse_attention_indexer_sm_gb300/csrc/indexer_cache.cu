@@ -13,7 +13,7 @@
 //   was bound by instructions (8192 x 64 rows of 128 in bf16: 60 us). The largest magnitude is
 //   found on the bit patterns, as integers, which order a NaN above everything. Reading back, a lane
 //   makes one 32-byte store of 16 or 8 columns; eight CTAs an SM hide the loads' latency, which four rows in
-//   flight in each of fewer lanes did not (524288 rows of 512 to bf16: 140 against 203 us).
+//   flight in each of fewer lanes did not (524288 rows of 512 to bf16: 132 against 203 us).
 
 #include <cuda_fp8.h>
 
@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     const uint32_t row = live ? quotient(p.blocks, u) : 0;
     const uint32_t kb = live ? u - row * p.blocks.d : 0;
     const int cols = live ? min(p.dim - static_cast<int>(kb) * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
+    int32_t slot_id = -1;
+    if constexpr (SLOTS) slot_id = live ? p.slots[row] : -1;  // on its way with the row
     const uint32_t t = quotient(p.heads, row);
     const T* src = x + t * p.x_ts + (row - t * p.heads.d) * p.x_hs + kb * INDEXER_BLOCK;
 #pragma unroll
@@ -163,10 +165,9 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     uint8_t* code;
     float* scale_at;
     if constexpr (SLOTS) {
-      const int32_t s = p.slots[row];
-      const uint32_t slot = static_cast<uint32_t>(s);
+      const uint32_t slot = static_cast<uint32_t>(slot_id);
       if (slot >= p.capacity) {  // negative ones too
-        if (s != -1 && lane == 0 && kb == 0) atomicAdd(&g_guard_hits, 1u);
+        if (slot_id != -1 && lane == 0 && kb == 0) atomicAdd(&g_guard_hits, 1u);
         continue;
       }
       const uint32_t page = quotient(p.page_size, slot), off = slot - page * p.page_size.d;
@@ -283,15 +284,18 @@ __global__ void __launch_bounds__(kThreads, 8) read_kernel(const ReadParams p) {
   }
 }
 
-unsigned grid_for(int64_t threads, int64_t most) {
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+// Four times the CTAs that an SM holds, at most: enough rounds to even out uneven ones, few enough to keep a CTA's start
+// cheap (65535 rows of 576 written: 23.3 us with one time, 22.1 with four, 23.4 with eight; 524288 rows of 512 read: 140 us
+// with two, 132 with four).
+unsigned grid_for(int64_t threads, int sms) {
+  const int64_t blocks = (threads + kThreads - 1) / kThreads, most = int64_t(sms) * 32;
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 template <typename T>
 cudaError_t launch_quantise(const QuantParams& p, bool vec, int sms, cudaStream_t stream) {
   constexpr int64_t kWarpUnits = 32 / kBlockLanes;
-  const unsigned grid = grid_for((static_cast<int64_t>(p.units) + kWarpUnits - 1) / kWarpUnits * 32, int64_t(sms) * 8);
+  const unsigned grid = grid_for((static_cast<int64_t>(p.units) + kWarpUnits - 1) / kWarpUnits * 32, sms);
   if (p.slots != nullptr)
     return vec ? launch(quantise_kernel<T, true, true>, grid, kThreads, 0, stream, p)
                : launch(quantise_kernel<T, false, true>, grid, kThreads, 0, stream, p);
@@ -344,8 +348,7 @@ int run_quantise(QuantParams p, int32_t dtype, int64_t tokens, int64_t heads, cu
 
 template <typename T>
 cudaError_t launch_read(const ReadParams& p, bool vec, int sms, cudaStream_t stream) {
-  // twice the CTAs that fit: a CTA's rows are far apart, and uneven in time
-  const unsigned grid = grid_for(p.units, int64_t(sms) * 16);
+  const unsigned grid = grid_for(p.units, sms);
   return vec ? launch(read_kernel<T, 32 / sizeof(T)>, grid, kThreads, 0, stream, p)
              : launch(read_kernel<T, 1>, grid, kThreads, 0, stream, p);
 }

@@ -794,3 +794,23 @@ def test_scores_of_drawn_shapes(fw, seed):
     q, w, codes, scales, table, lens, _ = args
     for i in {0, b // 2, b - 1}:
         check_scores(got[i * n:(i + 1) * n], q[i:i + 1], w[i:i + 1], codes, scales, table[i:i + 1], lens[i:i + 1], row_len)
+
+
+def test_calls_on_two_streams_at_once(fw):
+    """Scores and writes of two independent streams, overlapping in time, give what each gives alone."""
+    jobs = []
+    for seed, case in ((21, (150, 1, 64, 900, 64)), (22, (3, 40, 64, 2000, 64))):
+        args = scores_inputs(seed, *case)
+        x = torch.randn((5000, 128), generator=gen(seed)).to(torch.bfloat16).cuda()
+        jobs.append((args, x, fw.indexer_scores(*args), fw.indexer_quantise(x), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for k, (args, x, _, _, stream) in enumerate(jobs):
+            with torch.cuda.stream(stream):
+                got[k].append((fw.indexer_scores(*args), fw.indexer_quantise(x)))
+    torch.cuda.synchronize()
+    for k, (_, _, scores, (codes, scales), _) in enumerate(jobs):
+        for s, (c, f) in got[k]:
+            assert torch.equal(s, scores) and torch.equal(f, scales)
+            assert torch.equal(c.view(torch.uint8), codes.view(torch.uint8))
