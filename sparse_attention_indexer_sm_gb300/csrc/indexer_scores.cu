@@ -725,6 +725,8 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&key_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&query_map) : "memory");
     for (int i = 0; i < kKeyStages; ++i) {
       bar_init(&s.key_full[i], 1);
       bar_init(&s.key_empty[i], P::kMultipliers);
