@@ -814,3 +814,27 @@ def test_calls_on_two_streams_at_once(fw):
         for s, (c, f) in got[k]:
             assert torch.equal(s, scores) and torch.equal(f, scales)
             assert torch.equal(c.view(torch.uint8), codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("case", [(64, 1, 64, 12000, 64), (1, 1, 64, 700000, 64), (40, 3, 64, 16000, 64), (9, 60, 32, 9000, 64),
+                                  (300, 1, 24, 3000, 16), (2, 40, 128, 40000, 64), (700, 1, 8, 1100, 1)])
+def test_scores_in_spans(fw, case):
+    """Calls large enough that CTAs share the tiles out by the rows' lengths: mostly short rows, some empty, a few full;
+    all rows empty; only the last one not."""
+    b, n, _, row_len, _ = case
+    g = gen(sum(case))
+    short = (torch.rand((b, n), generator=g) ** 4 * row_len).int()
+    full = torch.rand((b, 1), generator=g) < 0.1
+    last = torch.zeros((b, n), dtype=torch.int32)
+    last[-1, -1] = row_len - 3
+    steps = (row_len - n + 1 + torch.arange(n, dtype=torch.int32)).clamp(min=0).expand(b, n).contiguous()
+    for lens in (torch.where(full, row_len, short).int(), torch.zeros((b, n), dtype=torch.int32), last, steps):
+        q, w, codes, scales, table, lens, _ = scores_inputs(sum(case), *case, lens=lens.tolist())
+        got = fw.indexer_scores(q, w, codes, scales, table, lens, row_len)
+        seen = torch.arange(row_len).cuda() < lens.view(-1, 1)
+        assert torch.equal(got == -math.inf, ~seen)
+        for i in range(0, b, max(1, b // 5)):  # a few at a time they are items in turn
+            few = fw.indexer_scores(q[i:i + 1], w[i:i + 1], codes, scales, table[i:i + 1], lens[i:i + 1], row_len)
+            assert torch.equal(got[i * n:(i + 1) * n], few)
+        small = slice(0, min(n, 4))
+        check_scores(got[small], q[:1, small], w[:1, small], codes, scales, table[:1], lens[:1, small], row_len)
