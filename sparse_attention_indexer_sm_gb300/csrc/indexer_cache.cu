@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     const int cols = live ? min(p.dim - static_cast<int>(kb) * INDEXER_BLOCK, INDEXER_BLOCK) : 0;
     int32_t slot_id = -1;
     if constexpr (SLOTS) slot_id = live ? p.slots[row] : -1;  // on its way with the row
-    const uint32_t t = quotient(p.heads, row);
-    const T* src = x + t * p.x_ts + (row - t * p.heads.d) * p.x_hs + kb * INDEXER_BLOCK;
+    const uint32_t t = SLOTS ? row : quotient(p.heads, row);  // a cache's rows have no heads
+    const T* src = x + t * p.x_ts + (SLOTS ? 0 : (row - t * p.heads.d) * p.x_hs) + kb * INDEXER_BLOCK;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) bits[i] = 0;
     if constexpr (VEC) {

@@ -1078,11 +1078,12 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   }
   p.items = p.slices * ((p.tiles + p.chunk - 1) / p.chunk);
   // Equal spans of the tiles that are seen, whatever the lengths, instead of items in turn: adding the lengths up costs
-  // 1.7 us, so from 32 tiles an SM on, were all rows full. Lengths even over the range: 64 rows of up to 32768 keys 30
+  // 1.7 us, so from 32 tiles an SM on, were all rows full, and from more with more slices than a CTA's threads read at
+  // once. Lengths even over the range: 64 rows of up to 32768 keys 30
   // against 41 us, 256 rows 99 against 134, 8 of up to 262144 30 against 39 (48 of up to 8192, 20 tiles an SM: 11.2
   // against 10.7); full rows, 4 of 262144 28.6 against 26.9, 256 of 32768 176 against 178.
   const bool spans = p.slices <= kMaxSpanSlices && p.slices * (p.tiles + kItemCost) <= INT32_MAX &&
-                     p.slices * p.tiles >= int64_t(sms) * 32;
+                     p.slices * p.tiles >= int64_t(sms) * (32 + p.slices / 64);
 
   CUtensorMap key_map, query_map;
   // a cache of no pages has none that passes the kernel's check: its map is never used
