@@ -12,7 +12,7 @@
 //   values what a lane does once a block (its place, its scale) cost as much as its values, and the kernel
 //   was bound by instructions (8192 x 64 rows of 128 in bf16: 60 us). The largest magnitude is
 //   found on the bit patterns, as integers, which order a NaN above everything. Reading back, a lane
-//   makes one 32-byte store of 16 or 8 columns; eight CTAs an SM hide the loads' latency, which four rows in
+//   makes one 32-byte store of 16 or 8 columns (or 16-byte store of 8); eight CTAs an SM hide the loads' latency, which four rows in
 //   flight in each of fewer lanes did not (524288 rows of 512 to bf16: 132 against 203 us).
 
 #include <cuda_fp8.h>
@@ -248,7 +248,7 @@ struct ReadParams {
   int32_t dim;
 };
 
-// An item is V columns of a row: V * sizeof(T) = 32 bytes of output in one store, or one column (V = 1).
+// An item is V columns of a row: V * sizeof(T) = 32 or 16 bytes of output in one store, or one column (V = 1).
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 8) read_kernel(const ReadParams p) {
   begin_after_prior_grids();
@@ -277,9 +277,15 @@ __global__ void __launch_bounds__(kThreads, 8) read_kernel(const ReadParams p) {
         y[2 * i] = from_float<T>(v.x * f);
         y[2 * i + 1] = from_float<T>(v.y * f);
       }
-      uint32_t words[8];
-      memcpy(words, y, sizeof(words));
-      store32(dst, words);
+      if constexpr (V * sizeof(T) == 32) {
+        uint32_t words[8];
+        memcpy(words, y, sizeof(words));
+        store32(dst, words);
+      } else {
+        uint4 words;
+        memcpy(&words, y, sizeof(words));
+        *reinterpret_cast<uint4*>(dst) = words;
+      }
     }
   }
 }
@@ -347,10 +353,14 @@ int run_quantise(QuantParams p, int32_t dtype, int64_t tokens, int64_t heads, cu
 }
 
 template <typename T>
-cudaError_t launch_read(const ReadParams& p, bool vec, int sms, cudaStream_t stream) {
+cudaError_t launch_read(const ReadParams& p, int columns, int sms, cudaStream_t stream) {
   const unsigned grid = grid_for(p.units, sms);
-  return vec ? launch(read_kernel<T, 32 / sizeof(T)>, grid, kThreads, 0, stream, p)
-             : launch(read_kernel<T, 1>, grid, kThreads, 0, stream, p);
+  constexpr int kWide = 32 / sizeof(T);
+  if (columns == kWide) return launch(read_kernel<T, kWide>, grid, kThreads, 0, stream, p);
+  if constexpr (kWide > 8) {
+    if (columns == 8) return launch(read_kernel<T, 8>, grid, kThreads, 0, stream, p);
+  }
+  return launch(read_kernel<T, 1>, grid, kThreads, 0, stream, p);
 }
 
 bool dtype_ok(int32_t dtype) { return dtype >= INDEXER_BF16 && dtype <= INDEXER_FP32; }
@@ -452,18 +462,23 @@ int indexer_cache_read(const indexer_cache_t* cache, const int32_t* slots, int64
   p.scale_ps = cache->scale_page_stride;
   p.scale_ts = cache->scale_token_stride;
   p.capacity = static_cast<uint32_t>(cache->num_pages * cache->page_size);
-  const int32_t columns = 32 / static_cast<int32_t>(dtype_bytes(dtype));  // of a 32-byte store
-  const bool vec = p.dim % columns == 0 && p.code_ts % columns == 0 && p.code_ps % columns == 0 &&
-                   aligned(p.codes, columns) && aligned(out, 32);
-  const int32_t items = vec ? p.dim / columns : p.dim;
+  // Columns of an item: a 32-byte store where rows start on 32 bytes, or eight, or one (239616 rows of 200 to bf16: eight
+  // 27 us, one 111).
+  const int32_t wide = 32 / static_cast<int32_t>(dtype_bytes(dtype));
+  auto fits = [&](int32_t n) {
+    return p.dim % n == 0 && p.code_ts % n == 0 && p.code_ps % n == 0 && aligned(p.codes, n) &&
+           aligned(out, n * dtype_bytes(dtype));
+  };
+  const int32_t columns = fits(wide) ? wide : fits(8) ? 8 : 1;
+  const int32_t items = p.dim / columns;
   p.items = divisor(items);
   const int64_t step = rows_of_launch(items);
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t n = rows - r < step ? rows - r : step;
     p.units = static_cast<uint32_t>(n * items);
-    if (dtype == INDEXER_BF16) e = launch_read<__nv_bfloat16>(p, vec, sms, stream);
-    else if (dtype == INDEXER_FP16) e = launch_read<__half>(p, vec, sms, stream);
-    else e = launch_read<float>(p, vec, sms, stream);
+    if (dtype == INDEXER_BF16) e = launch_read<__nv_bfloat16>(p, columns, sms, stream);
+    else if (dtype == INDEXER_FP16) e = launch_read<__half>(p, columns, sms, stream);
+    else e = launch_read<float>(p, columns, sms, stream);
     if (e != cudaSuccess) return status_of(e);
     p.slots += n;
     p.out = static_cast<char*>(p.out) + n * p.dim * static_cast<int64_t>(dtype_bytes(dtype));
