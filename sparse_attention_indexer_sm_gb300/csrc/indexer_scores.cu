@@ -9,8 +9,8 @@
 //
 // What bounds it: one query a sequence (decode) reads 132 bytes a key for 2 * 128 * heads
 // operations and is bound by memory (256 rows of 32768 keys, 64 heads: 175 us, 6.5 TB/s); a prompt's chunk shares a
-// key tile between the queries of a group and is bound by the epilogue's relu-sum (2048 queries over 32768 keys: 548 us,
-// 2.01 PFLOP/s).
+// key tile between the queries of a group and is bound by the epilogue's relu-sum (2048 queries over 32768 keys: 512 us,
+// 2.14 PFLOP/s).
 //
 // One CTA an SM, persistent: over items (sequence, query group, chunk of tiles) in turn, or over an equal span of all tiles
 // that some query sees, which each CTA finds by adding up the lengths. A tile's products are one unit of columns, or
@@ -363,11 +363,10 @@ template <> struct Walk<true> {
   }
 };
 
-// The place of the item at w, or the one after it, and the load of its lengths: asked for one item ahead. Items in turn
-// are ordered with the chunk of tiles outermost, so that the CTAs work on the same tiles of a sequence at about the same
-// time and find them in L2.
+// The place of the item at w, or the one after it. Items in turn are ordered with the chunk of tiles outermost, so that
+// the CTAs work on the same tiles of a sequence at about the same time and find them in L2.
 template <bool kSpans>
-__device__ __forceinline__ Item item_at(const ScoresParams& p, const Walk<kSpans>& w, int ahead) {
+__device__ __forceinline__ Item place_at(const ScoresParams& p, const Walk<kSpans>& w, int ahead) {
   Item it = {};
   int64_t slice, c = 0;
   if constexpr (kSpans) {
@@ -385,6 +384,13 @@ __device__ __forceinline__ Item item_at(const ScoresParams& p, const Walk<kSpans
   it.query = r.query;
   it.first = static_cast<int32_t>(c) * p.chunk;
   it.end = min(it.first + p.chunk, p.tiles);
+  return it;
+}
+
+// The same and the load of its lengths: asked for one item ahead.
+template <bool kSpans>
+__device__ __forceinline__ Item item_at(const ScoresParams& p, const Walk<kSpans>& w, int ahead) {
+  Item it = place_at(p, w, ahead);
   const int lane = threadIdx.x & 31;
   if (lane < it.count) it.len = p.seq_lens[it.query + lane];
   return it;
@@ -715,7 +721,6 @@ __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, in
 struct Lane {
   float* out;            // this key's score of the warp's first query
   const int32_t* lens;   // of the warp's queries
-  int64_t row_len;
   uint32_t tmem_empty, next_full, next_phase;  // barriers: to be told that the tile is read; of the next unit
   uint32_t tmem;
   float scale;
@@ -726,39 +731,38 @@ struct Lane {
 // Columns from C * kLoad on, which are on their way to r. With registers for it (two epilogue groups) the next load is
 // sent off before they are summed: 64 or 128 heads 4% faster; of four groups, whose warps hide it from one another, after.
 // Whether the next unit is there already: asked before the last sums, for use after them.
-template <int kHeads, int kLoad, bool kWhole, int C, int kColumns>
-__device__ __forceinline__ bool columns_from(const Lane& l, const float (&w)[kColumns], float (&r)[kLoad],
-                                             uint64_t acc0, uint64_t acc1) {
+template <int kHeads, int kLoad, bool kWhole, int C, int kPairs>
+__device__ __forceinline__ bool columns_from(const ScoresParams& p, const Lane& l, const uint64_t (&w)[kPairs],
+                                             float (&r)[kLoad], uint64_t acc0, uint64_t acc1) {
+  constexpr int kColumns = 2 * kPairs;
   tmem_wait<kLoad>(r);
   auto add = [&]() {
 #pragma unroll
     for (int h = 0; h < kLoad / 4; ++h) {
-      constexpr int at = C * kLoad;
-      acc0 = fma2(pack2(fmaxf(r[4 * h], 0.0f), fmaxf(r[4 * h + 1], 0.0f)),
-                  pack2(w[at + 4 * h], w[at + 4 * h + 1]), acc0);
-      acc1 = fma2(pack2(fmaxf(r[4 * h + 2], 0.0f), fmaxf(r[4 * h + 3], 0.0f)),
-                  pack2(w[at + 4 * h + 2], w[at + 4 * h + 3]), acc1);
+      constexpr int at = C * kLoad / 2;
+      acc0 = fma2(pack2(fmaxf(r[4 * h], 0.0f), fmaxf(r[4 * h + 1], 0.0f)), w[at + 2 * h], acc0);
+      acc1 = fma2(pack2(fmaxf(r[4 * h + 2], 0.0f), fmaxf(r[4 * h + 3], 0.0f)), w[at + 2 * h + 1], acc1);
     }
     if constexpr ((C + 1) * kLoad % kHeads == 0) {
       constexpr int g = C * kLoad / kHeads;
       const float2 a = unpack2(add2(acc0, acc1));
       const float y = (a.x + a.y) * l.scale;
-      float* const out = l.out + g * l.row_len;
+      float* const out = l.out + g * p.row_len;
       if constexpr (kWhole) {
         *out = l.no_page ? __int_as_float(0xff800000) : y;
-      } else if (l.j < l.row_len) {
+      } else if (l.j < p.row_len) {
         *out = l.no_page || l.j >= l.lens[g] ? __int_as_float(0xff800000) : y;
       }
       acc0 = acc1 = 0;
     }
   };
   if constexpr ((C + 1) * kLoad < kColumns) {
-    if ((C + 1) * kLoad < l.columns) {
+    if ((kWhole && kColumns == 64) || (C + 1) * kLoad < l.columns) {
       float next[kLoad];
       if constexpr (kColumns == 64) add();
       tmem_load<kLoad>(l.tmem + (C + 1) * kLoad, next);
       if constexpr (kColumns != 64) add();
-      return columns_from<kHeads, kLoad, kWhole, C + 1>(l, w, next, acc0, acc1);
+      return columns_from<kHeads, kLoad, kWhole, C + 1>(p, l, w, next, acc0, acc1);
     }
   }
   // every column of the tile is in registers: its stage is free
@@ -792,7 +796,6 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     }
   };
   Lane l;
-  l.row_len = p.row_len;
   const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(tid & ~31) << 16) + (kGroups == 4 ? wg * kColumns : 0);
   // the group's TMEM stages: of two groups wg, wg + 2, ..., of four all of them
   constexpr uint32_t kStep = kGroups == 2 ? 2 : 1;
@@ -801,26 +804,35 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
   uint32_t tiles = 0, stage = first_stage, phase = 0;
   bool ready = false;
   Walk<kSpans> walk(s);
-  Item next_item = item_at(p, walk, 0);
-  weights_of(next_item);
+  int32_t next_len;  // the rest of the next item's place is worked out again: registers are short while tiles go by
+  {
+    const Item it = item_at(p, walk, 0);
+    next_len = it.len;
+    weights_of(it);
+  }
   for (; walk.more(p); walk.on()) {
-    Item it = next_item;
+    Item it = place_at(p, walk, 0);
+    it.len = next_len;
     item_ready(p, walk, it);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kBring; ++k) weights[lane + 32 * k] = bring[k];
     if (lane < it.count) s.lens[warp][lane] = it.len;
     __syncwarp();
-    float w[kColumns];
+    uint64_t w[kColumns / 2];  // in pairs
 #pragma unroll
     for (int k = 0; k < kColumns / 4; ++k) {
-      const float4 f = reinterpret_cast<const float4*>(weights)[k];
-      w[4 * k] = f.x, w[4 * k + 1] = f.y, w[4 * k + 2] = f.z, w[4 * k + 3] = f.w;
+      const ulonglong2 f = reinterpret_cast<const ulonglong2*>(weights)[k];
+      w[2 * k] = f.x, w[2 * k + 1] = f.y;
     }
     const int count = min(max(it.count - first, 0), kQueries);
     l.columns = count * kHeads;
+    // every query of the group sees every key of the tiles that start here or before; of four groups, if all its columns
+    // are in use: no look at their number at each load (2048 queries of 16 heads 154 -> 148 us)
+    const int whole = kGroups == 4 && count < kQueries ? -1 : it.shortest - kTile;
     l.lens = s.lens[warp] + first;
-    next_item = item_at(p, walk, 1);
+    const Item next_item = item_at(p, walk, 1);
+    next_len = next_item.len;
     weights_of(next_item);  // on their way while this item is worked on
     // The output's place goes on from tile to tile: worked out at each from a row's start, 2048 queries took 7% longer.
     const int step = tile_step<kGroups>(p), t0 = first_tile<kGroups>(p, it, wg, tiles);
@@ -848,12 +860,12 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
       l.no_page = __float_as_uint(l.scale) == kNoPage;
       l.next_full = full_base + 8 * stage;
       l.next_phase = phase;
-      // every query of the group sees every key of most tiles
-      const bool next = t * kTile <= it.shortest - kTile ? columns_from<kHeads, kLoad, true, 0>(l, w, r, 0, 0)
-                                                         : columns_from<kHeads, kLoad, false, 0>(l, w, r, 0, 0);
+      const bool next = t * kTile <= whole ? columns_from<kHeads, kLoad, true, 0>(p, l, w, r, 0, 0)
+                                           : columns_from<kHeads, kLoad, false, 0>(p, l, w, r, 0, 0);
       ready = __all_sync(0xffffffffu, next);
     }
     tiles += it.seen - it.first;
+    if constexpr (kSpans) continue;  // fill_rest's
     // tiles that no query of the group sees
     const bool in_turn = kGroups == 2 && p.units == 1;
     float* const out = p.out + (it.query + first) * p.row_len;
@@ -874,6 +886,17 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
 }
 
+// Whether the dynamic shared memory starts where its declared alignment says, which the swizzled tiles rely on. Without a
+// rounding of its address every place in it is a constant, and the registers that held addresses are the epilogue's
+// (2048 queries over 32768 keys, 64 heads: 548 -> 512 us).
+__device__ __forceinline__ bool aligned_base(const Shared& s) {
+  uint32_t base = smem_addr(&s);
+  asm volatile("" : "+r"(base));
+  if (base % 1024 == 0) return true;
+  if (threadIdx.x == 0) atomicAdd(&g_guard_hits, 1u);
+  return false;
+}
+
 // kHeads: heads rounded up to 16, 32, 64 or 128. The rounding's rows of B are zeros (beyond the
 // tensor map's heads) and their weights are 0.
 template <int kGroups, bool kSpans, int kHeads>
@@ -881,8 +904,9 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
     scores_kernel(const ScoresParams p, const __grid_constant__ CUtensorMap key_map,
                   const __grid_constant__ CUtensorMap query_map) {
   using P = Plan<kGroups>;
-  extern __shared__ uint8_t raw[];
-  Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Shared& s = *reinterpret_cast<Shared*>(raw);
+  if (!aligned_base(s)) return;
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&key_map) : "memory");
@@ -945,7 +969,7 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
 }
 
-constexpr size_t kSmemBytes = sizeof(Shared) + 1024;
+constexpr size_t kSmemBytes = sizeof(Shared);
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
