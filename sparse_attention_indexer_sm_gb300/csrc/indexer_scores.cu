@@ -24,10 +24,11 @@
 // in one of two plans. A lone warp takes some 50 cycles for each barrier that it looks at, so with up to 128 columns, where
 // a tile is soon done, every role that a tile passes through has two warps or four that take turns. With more
 // columns an epilogue group's work on a tile outlasts that, and what counts is how many warps hide each other's latencies: four
-// groups, of a quarter of the columns each (2048 queries over 32768 keys, 16 and 64 heads: 170 and 588 us against
-// 192 and 617 with two groups). There the epilogue still bounds the kernel, at 63% of the issue slots and 60% of the
-// integer pipe (relu is one of its instructions); the tensor pipe is at 37%. Moving half of the relus to the fp32 pipe (a
-// saturating product) changed nothing, nor did larger or fewer loads from TMEM: what is left is latency.
+// groups, of a quarter of the columns each (2048 queries over 32768 keys, 16 and 64 heads: 147 and 511 us against
+// 183 and 544 with two groups). There the epilogue still bounds the kernel, at 66% of the issue slots and 64% of the
+// integer pipe (relu is one of its instructions); the tensor pipe is at 43%. Its warps wait for a tile 5% of their time;
+// of some 200 instructions a warp and tile 96 are relus and products. Moving half of the relus to the fp32 pipe (a
+// saturating product) changed nothing, nor did larger or smaller loads from TMEM: what is left is latency.
 // A barrier's parity tells a phase from the next one, but not from the one after that. So each place of a
 // ring belongs to the same warp of a role throughout: tiles and units are dealt out by their running
 // numbers over the whole launch, and the rings' lengths are multiples of the numbers of warps.
@@ -1085,7 +1086,8 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   p.groups = (queries + p.group - 1) / p.group;
   p.tiles = static_cast<int32_t>((row_len + kTile - 1) / kTile);
   // Groups of queries of more than 128 columns, in columns of 16, 32 or 64 a query: four epilogue groups, a quarter of a
-  // tile's columns each, and one unit a tile; otherwise two, and units of up to 128 columns.
+  // tile's columns each, and one unit a tile; otherwise two, and units of up to 128 columns. (64 rows of 4 queries of 64
+  // heads, 32768 keys: 76 us with four, 79 with two.)
   const int columns = p.group * head_rows;
   const int epilogues = columns > 128 && head_rows <= 64 ? 4 : 2;
   p.unit_queries = epilogues == 4 ? p.group : Plan<2>::kColumns / head_rows;
