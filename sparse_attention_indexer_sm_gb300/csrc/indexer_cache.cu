@@ -490,7 +490,9 @@ int indexer_guard_hits(uint64_t* hits) {
   using namespace indexer_gb300;
   if (hits == nullptr) return TOPK_ERR_INVALID_ARGUMENT;
   unsigned int a = 0, b = 0;
-  cudaError_t e = cache_guard_hits(&a);
+  // the copies below are ordered behind the default stream alone, not behind non-blocking ones
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cache_guard_hits(&a);
   if (e == cudaSuccess) e = scores_guard_hits(&b);
   if (e == cudaSuccess) *hits = static_cast<uint64_t>(a) + b;
   return status_of(e);
@@ -498,7 +500,8 @@ int indexer_guard_hits(uint64_t* hits) {
 
 int indexer_reset_guard_hits(void) {
   using namespace indexer_gb300;
-  cudaError_t e = reset_cache_guard_hits();
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = reset_cache_guard_hits();
   if (e == cudaSuccess) e = reset_scores_guard_hits();
   return status_of(e);
 }
