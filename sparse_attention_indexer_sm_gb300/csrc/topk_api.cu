@@ -516,7 +516,9 @@ int topk_guard_hits(uint64_t* hits) {
   int st = device_state(&ds);
   if (st != TOPK_OK) return st;
   unsigned int a = 0, b = 0;
-  cudaError_t e = topk_gb300::cta512::guard_hits(&a);
+  // the copies below are ordered behind the default stream alone, not behind non-blocking ones
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = topk_gb300::cta512::guard_hits(&a);
   if (e == cudaSuccess) e = topk_gb300::cta256::guard_hits(&b);
   if (e != cudaSuccess) return fail_cuda(e);
   *hits = static_cast<uint64_t>(a) + b;
@@ -527,7 +529,8 @@ int topk_reset_guard_hits(void) {
   DeviceState* ds = nullptr;
   int st = device_state(&ds);
   if (st != TOPK_OK) return st;
-  cudaError_t e = topk_gb300::cta512::reset_guard_hits();
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = topk_gb300::cta512::reset_guard_hits();
   if (e == cudaSuccess) e = topk_gb300::cta256::reset_guard_hits();
   return e == cudaSuccess ? TOPK_OK : fail_cuda(e);
 }

@@ -58,3 +58,31 @@ def test_count_waits_for_other_streams(fw):
     fw.indexer_reset_guard_hits()
     torch.cuda.synchronize()
     assert fw.indexer_guard_hits() == 0
+
+
+def test_topk_count_waits_for_other_streams(fw):
+    """The same of the top-k's count: a row that needs more pages than its table's stride (through the C
+    ABI, as the binding refuses such a table)."""
+    lib = fw.load_library()
+    n, size, pages, k = 8192, 64, 100, 64
+    scores = torch.randn((2, n), generator=gen(1)).cuda()
+    lens = torch.tensor([n, 6400], dtype=torch.int32, device="cuda")
+    table = torch.arange(2 * pages, dtype=torch.int32, device="cuda").view(2, pages)
+    out = torch.empty((2, k), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def call():
+        torch.cuda._sleep(LONG)
+        st = lib.topk_transform_paged(scores.data_ptr(), n, lens.data_ptr(), table.data_ptr(), pages, size, 2, k,
+                                      out.data_ptr(), None, 0, side.cuda_stream)
+        assert st == 0
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call()
+    assert fw.topk_guard_hits() == 1
+    with torch.cuda.stream(side):
+        call()
+    fw.topk_reset_guard_hits()
+    torch.cuda.synchronize()
+    assert fw.topk_guard_hits() == 0
