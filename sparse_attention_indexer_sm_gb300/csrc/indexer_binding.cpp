@@ -104,9 +104,18 @@ cudaStream_t stream_of(const Stream& stream, const Tensor& x) {
   return stream ? reinterpret_cast<cudaStream_t>(*stream) : c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
 }
 
-Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& x) {
+// An output. Of a call on a stream of the caller's it comes from that stream's memory: a block of the current stream's may
+// still be in use by work queued there, which `stream` is not behind. The current stream, where the caller goes on, counts
+// as a user of it: work queued there holds the block when the caller lets go of it.
+Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& x, const Stream& stream) {
   // straight from the caching allocator: at::empty's way through the dispatcher takes longer than the checks
-  return at::detail::empty_cuda(shape, type, x.device(), std::nullopt);
+  if (!stream) return at::detail::empty_cuda(shape, type, x.device(), std::nullopt);
+  const c10::DeviceIndex device = x.device().index();
+  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device);
+  const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream_of(stream, x), device));
+  Tensor t = at::detail::empty_cuda(shape, type, x.device(), std::nullopt);
+  t.record_stream(current);
+  return t;
 }
 
 // ---------------------------------------------------------------- rotary positions
@@ -131,7 +140,7 @@ struct Rotary : torch::autograd::Function<Rotary> {
     ctx->saved_data["start"] = start;
     ctx->saved_data["scale"] = scale;
     ctx->saved_data["transpose"] = transpose;
-    Tensor out = fresh(x.sizes(), x.scalar_type(), x);
+    Tensor out = fresh(x.sizes(), x.scalar_type(), x, Stream());
     run_rotary(x, rows_of(x, "x"), positions, freqs, static_cast<int>(layout), start, scale, transpose, out, Stream());
     return out;
   }
@@ -182,7 +191,7 @@ Tensor rotary(const Tensor& x, const Tensor& positions, const Tensor& freqs, int
       require(a.first >= b.second || b.first >= a.second, "out must be x itself or not overlap it");
     }
   } else {
-    y = fresh(x.sizes(), x.scalar_type(), x);
+    y = fresh(x.sizes(), x.scalar_type(), x, stream);
   }
   run_rotary(x, r, positions, freqs, layout, start, scale, transpose, y, stream);
   return y;
@@ -208,8 +217,8 @@ std::pair<Tensor, Tensor> quantise(const Tensor& x, int format, const std::optio
   }
   if (codes) check_contiguous(*codes, "codes", ScalarType::Float8_e4m3fn, x.sizes(), x);
   if (scales) check_contiguous(*scales, "scales", ScalarType::Float, shape, x);
-  Tensor c = codes ? *codes : fresh(x.sizes(), ScalarType::Float8_e4m3fn, x);
-  Tensor s = scales ? *scales : fresh(shape, ScalarType::Float, x);
+  Tensor c = codes ? *codes : fresh(x.sizes(), ScalarType::Float8_e4m3fn, x, stream);
+  Tensor s = scales ? *scales : fresh(shape, ScalarType::Float, x, stream);
   const c10::cuda::CUDAGuard guard(x.device());
   check_status(indexer_quantise(x.data_ptr(), r.ts, r.hs, r.dtype, r.tokens, static_cast<int32_t>(r.heads),
                                 static_cast<int32_t>(r.dim), format, weights ? weights->data_ptr<float>() : nullptr,
@@ -277,7 +286,7 @@ Tensor cache_read(const Tensor& codes, const Tensor& scales, const Tensor& slots
   c10::SmallVector<int64_t, 4> shape(slots.sizes().begin(), slots.sizes().end());
   shape.push_back(cache.dim);
   if (out) check_contiguous(*out, "out", kTypes[dtype], shape, codes);
-  Tensor y = out ? *out : fresh(shape, kTypes[dtype], codes);
+  Tensor y = out ? *out : fresh(shape, kTypes[dtype], codes, stream);
   const c10::cuda::CUDAGuard guard(codes.device());
   check_status(indexer_cache_read(&cache, slots.data_ptr<int32_t>(), slots.numel(), dtype, y.data_ptr(),
                                   stream_of(stream, codes)),
@@ -315,7 +324,7 @@ Tensor scores(const Tensor& q, const Tensor& weights, const Tensor& codes, const
   check_contiguous(seq_lens, "seq_lens", ScalarType::Int, {batch, queries}, q);
   const int64_t shape[2] = {batch * queries, row_len};
   if (out) check_contiguous(*out, "out", ScalarType::Float, shape, q);
-  Tensor y = out ? *out : fresh(shape, ScalarType::Float, q);
+  Tensor y = out ? *out : fresh(shape, ScalarType::Float, q, stream);
   const c10::cuda::CUDAGuard guard(q.device());
   check_status(indexer_scores(static_cast<const uint8_t*>(q.data_ptr()), weights.data_ptr<float>(), &cache,
                               page_table.data_ptr<int32_t>(), pt_stride, seq_lens.data_ptr<int32_t>(),

@@ -3,7 +3,8 @@
 A thin binding over the C ABI in ``include/indexer_ops.h``, in the manner of the
 package's top-k calls: tensors are checked and marshalled (in ``csrc/indexer_binding.cpp``),
 the work runs in the library's sm_103a kernels on the tensors' device and the current torch
-stream (or ``stream``), and nothing falls back to torch. A decode step, with a paged cache
+stream (or ``stream``, which the caller orders behind the work that makes the inputs), and
+nothing falls back to torch. A decode step, with a paged cache
 ``codes`` [pages, page_size, 128] (float8_e4m3fn) and ``scales`` [pages, page_size, 1]:
 
     freqs, scale = indexer_rotary_freqs(64, device="cuda")
@@ -99,10 +100,10 @@ def _choice(value, table, name: str) -> int:
 
 
 def _on(stream, call, *args):
-    """A call on a stream of the caller's. Its tensors, given or made by it, are in use there until its kernel has
-    ended: none of their memory is handed out again before that."""
+    """A call on a stream of the caller's. Its tensors are in use there until its kernel has ended: none of their memory
+    is handed out again before that. (Outputs that it makes come from that stream's memory.)"""
     out = call(*args, stream.cuda_stream)
-    for t in (*args, *(out if isinstance(out, tuple) else (out,))):
+    for t in args:
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
     return out

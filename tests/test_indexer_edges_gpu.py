@@ -86,3 +86,74 @@ def test_topk_count_waits_for_other_streams(fw):
     fw.topk_reset_guard_hits()
     torch.cuda.synchronize()
     assert fw.topk_guard_hits() == 0
+
+
+# ---------------------------------------------------------------- outputs on other streams
+
+def pending_block(nbytes):
+    """Frees a block of the current stream's pool that queued work has still to write; its address."""
+    block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(LONG)
+    block.fill_(0x5A)
+    return block.data_ptr()
+
+
+def on_side_calls(fw):
+    """(name, bytes of each output, call) of everything that makes its own outputs, on inputs that are ready."""
+    g = gen(2)
+    n, k, size = 1000, 50, 20
+    x = torch.randn((200, 8, 128), generator=g).to(torch.bfloat16).cuda()
+    positions = torch.arange(200, dtype=torch.int32).cuda()
+    freqs, _ = fw.indexer_rotary_freqs(64)
+    codes, scales = make_cache(200, size)
+    flat = torch.randperm(200 * size, generator=g).int().cuda()
+    fw.indexer_cache_write(torch.randn((200 * size, 128), generator=g).cuda(), flat, codes, scales)
+    q, w = fw.indexer_quantise(x[:4], weights=torch.ones((4, 8), device="cuda"))
+    table = torch.randperm(200, generator=g).int().cuda().view(4, 50)
+    lens = torch.tensor([1000, 1, 500, 999], dtype=torch.int32).cuda()
+    return [
+        ("rotary", [x.numel() * 2], lambda **kw: (fw.indexer_rotary(x, positions, freqs, **kw),)),
+        ("quantise", [x.numel(), 200 * 8 * 4], lambda **kw: fw.indexer_quantise(x, **kw)),
+        ("read", [flat.numel() * 128 * 2], lambda **kw: (fw.indexer_cache_read(codes, scales, flat, **kw),)),
+        ("scores", [4 * n * 4], lambda **kw: (
+            fw.indexer_scores(q[:, None], w[:, None], codes, scales, table, lens[:, None], n, **kw),)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_output_made_on_another_stream(fw, which):
+    """A call on a stream that is not behind the current one: its output is no block that work queued on the
+    current stream has still to write."""
+    name, sizes, call = on_side_calls(fw)[which]
+    want = call()
+    side = torch.cuda.Stream()
+    call(stream=side)  # loads what is loaded once
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    pending = {pending_block(nbytes) for nbytes in sizes}
+    got = call(stream=side)
+    assert not pending & {t.data_ptr() for t in got}, name
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), name
+
+
+def test_output_read_on_the_current_stream_and_dropped(fw):
+    """An output that work queued on the current stream still reads is not handed out again to the stream it
+    was made on."""
+    x = torch.ones((4096, 128), device="cuda")
+    positions = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    freqs, _ = fw.indexer_rotary_freqs(64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = fw.indexer_rotary(x, positions, freqs, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(LONG)
+    seen = y.clone()
+    at = y.data_ptr()
+    del y
+    with torch.cuda.stream(side):
+        other = torch.full((4096, 128), 9.0, device="cuda")
+        assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(seen, x)
