@@ -140,9 +140,24 @@ def _vector(t: torch.Tensor, name: str, n: int, device) -> None:
         raise ValueError(f"{name} must be a contiguous int32 vector of length {n}")
 
 
-def _out(out, batch: int, k: int, device) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory that a call on ``stream`` (None: the current one) writes, from that stream's
+    pool: a block of the current stream's may still be in use by work queued there, which
+    another stream is not behind."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(out, batch: int, k: int, device, stream) -> torch.Tensor:
     if out is None:
-        return torch.empty((batch, k), dtype=torch.int32, device=device)
+        out = _empty((batch, k), torch.int32, device, stream)
+        if stream is not None:  # the caller goes on with it on the current stream
+            out.record_stream(torch.cuda.current_stream(device))
+        return out
     _cuda_tensor(out, "out", torch.int32, device)
     if tuple(out.shape) != (batch, k) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous int32 tensor of shape ({batch}, {k})")
@@ -166,9 +181,7 @@ def _workspace(lib, workspace, batch: int, max_row_len: int, k: int, device, str
         nbytes = int(lib.topk_workspace_bytes(batch, max_row_len, k))
     if nbytes == 0:
         return None, 0, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)  # in use on that stream until the call's kernels end
+    ws = _empty(nbytes, torch.uint8, device, stream)
     return ws.data_ptr(), nbytes, ws
 
 
@@ -192,7 +205,7 @@ def topk_transform_raw(scores: torch.Tensor, seq_lens: torch.Tensor, k: int,
     batch, row_stride = _scores_2d(scores)
     dev = scores.device
     _vector(seq_lens, "seq_lens", batch, dev)
-    out = _out(out, batch, k, dev)
+    out = _out(out, batch, k, dev, stream)
     ws, ws_bytes, _keep = _workspace(lib, workspace, batch, row_stride, k, dev, stream)
     with torch.cuda.device(dev):
         st = lib.topk_transform_raw(scores.data_ptr(), row_stride, seq_lens.data_ptr(), batch, k,
@@ -219,7 +232,7 @@ def topk_transform_paged(scores: torch.Tensor, seq_lens: torch.Tensor, page_tabl
         raise ValueError("page_table rows must not overlap (use .contiguous() on expanded tables)")
     if page_table.shape[1] * page_size < min(row_stride, scores.shape[1]):
         raise ValueError("page_table has too few pages for the rows")
-    out = _out(out, batch, k, dev)
+    out = _out(out, batch, k, dev, stream)
     ws, ws_bytes, _keep = _workspace(lib, workspace, batch, row_stride, k, dev, stream)
     with torch.cuda.device(dev):
         st = lib.topk_transform_paged(scores.data_ptr(), row_stride, seq_lens.data_ptr(),
@@ -242,7 +255,7 @@ def topk_transform_ragged(scores: torch.Tensor, row_starts: torch.Tensor, seq_le
     batch = int(row_starts.shape[0]) if row_starts.dim() == 1 else -1
     _vector(row_starts, "row_starts", batch, dev)
     _vector(seq_lens, "seq_lens", batch, dev)
-    out = _out(out, batch, k, dev)
+    out = _out(out, batch, k, dev, stream)
     ws, ws_bytes, _keep = _workspace(lib, workspace, batch, int(max_row_len_hint), k, dev, stream)
     with torch.cuda.device(dev):
         st = lib.topk_transform_ragged(scores.data_ptr(), row_starts.data_ptr(),
@@ -264,7 +277,7 @@ def topk_transform_window(scores: torch.Tensor, starts: torch.Tensor, seq_lens: 
     dev = scores.device
     _vector(starts, "starts", batch, dev)
     _vector(seq_lens, "seq_lens", batch, dev)
-    out = _out(out, batch, k, dev)
+    out = _out(out, batch, k, dev, stream)
     hint = int(max_row_len_hint) if 0 < int(max_row_len_hint) < row_stride else row_stride
     ws, ws_bytes, _keep = _workspace(lib, workspace, batch, hint, k, dev, stream)
     with torch.cuda.device(dev):
@@ -353,7 +366,7 @@ def topk_transform_grouped(problems: list[dict], stream=None, static_workspace: 
             _vector(q["starts"], "starts", batch, d)
             arr[i].row_starts = q["starts"].data_ptr()
             arr[i].max_row_len_hint = int(q.get("max_row_len_hint", 0))
-        out = _out(q.get("out"), batch, k, d)
+        out = _out(q.get("out"), batch, k, d, stream)
         vals = q.get("values")
         if vals is not None:
             _cuda_tensor(vals, "values", torch.float32, d)
@@ -384,12 +397,10 @@ def topk_transform_grouped(problems: list[dict], stream=None, static_workspace: 
         _check(st, "topk_transform_grouped")
         return outs
     with torch.cuda.device(dev):
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        ws = _empty(ws_bytes, torch.uint8, dev, stream) if ws_bytes else None
         st = lib.topk_transform_grouped(ctypes.addressof(arr), len(problems),
                                         ws.data_ptr() if ws is not None else None, ws_bytes,
                                         _stream(stream, dev))
-        if ws is not None:  # the launches on `stream` read it until they finish
-            ws.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
     _check(st, "topk_transform_grouped")
     return outs
 

@@ -157,3 +157,48 @@ def test_output_read_on_the_current_stream_and_dropped(fw):
         assert other.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(seen, x)
+
+
+@pytest.mark.parametrize("which", ["raw", "paged", "ragged", "window", "grouped", "sorted", "split"])
+def test_topk_output_made_on_another_stream(fw, which):
+    """The same of the top-k's calls, their workspaces among them."""
+    b, n, k = 8, 4000, 64
+    scores = torch.randn((b, n), generator=gen(6)).cuda()
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    starts = (torch.arange(b, dtype=torch.int32) * n).cuda()
+    table = torch.arange(b * 125, dtype=torch.int32, device="cuda").view(b, 125)
+    problem = {"form": "raw", "k": k, "scores": scores, "seq_lens": lens, "sorted": which == "sorted"}
+    calls = {
+        "raw": lambda **kw: fw.topk_transform_raw(scores, lens, k, **kw),
+        "paged": lambda **kw: fw.topk_transform_paged(scores, lens, table, 32, k, **kw),
+        "ragged": lambda **kw: fw.topk_transform_ragged(scores.view(-1), starts, lens, k, **kw),
+        "window": lambda **kw: fw.topk_transform_window(scores, torch.zeros_like(lens), lens, k, **kw),
+        "grouped": lambda **kw: fw.topk_transform_grouped([problem], **kw)[0],
+        "sorted": lambda **kw: fw.topk_transform_grouped([problem], **kw)[0],
+        "split": lambda **kw: fw.topk_transform_raw(scores, lens, k, **kw),
+    }
+    before = fw.topk_set_chip_split(2 if which == "split" else 1)
+    try:
+        call, spare = calls[which], fw.topk_workspace_bytes(b, n, k) if which == "split" else 0
+        want = call().sort(1).values
+        side = torch.cuda.Stream()
+        call(stream=side)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        pending = {pending_block(nbytes) for nbytes in (b * k * 4, max(spare, 1 << 16))}
+        got = call(stream=side)
+        assert got.data_ptr() not in pending
+        torch.cuda.synchronize()
+        assert torch.equal(got.sort(1).values, want)
+        with torch.cuda.stream(side):  # an output dropped while the current stream still reads it
+            torch.cuda._sleep(1)
+        side.synchronize()
+        torch.cuda._sleep(LONG)
+        seen, at = got.clone(), got.data_ptr()
+        del got
+        with torch.cuda.stream(side):
+            assert torch.zeros((b, k), dtype=torch.int32, device="cuda").data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(seen.sort(1).values, want)
+    finally:
+        fw.topk_set_chip_split(before)
