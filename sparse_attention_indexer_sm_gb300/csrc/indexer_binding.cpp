@@ -5,11 +5,13 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <initializer_list>
 #include <optional>
 #include <sstream>
 #include <stdexcept>
@@ -76,6 +78,16 @@ void check_vector(const Tensor& t, const char* name, ScalarType type, int64_t n,
   if (t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
     throw py::value_error(text(name, " must be a contiguous vector of length ", n));
 }
+
+// No operator has a forward-mode derivative: a tangent is refused, not dropped.
+void check_no_tangent(std::initializer_list<const Tensor*> tensors) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  for (const Tensor* t : tensors)
+    if (t != nullptr && t->_fw_grad(/*level=*/0).defined())
+      throw py::value_error("no forward-mode derivative: a tensor of the call carries a tangent");
+}
+
+const Tensor* given(const std::optional<Tensor>& t) { return t ? &*t : nullptr; }
 
 // [tokens, dim] or [tokens, heads, dim] with unit column stride.
 struct Rows {
@@ -175,6 +187,7 @@ Tensor rotary(const Tensor& x, const Tensor& positions, const Tensor& freqs, int
           "freqs must be a contiguous fp64 vector of at least one frequency");
   if (start < 0 || start > r.dim || 2 * freqs.size(0) > r.dim - start)
     throw py::value_error(text("columns [", start, ", ", start + 2 * freqs.size(0), ") do not lie within the row of ", r.dim));
+  check_no_tangent({&x, given(out)});
   const bool recording = at::GradMode::is_enabled();
   if (recording && x.requires_grad()) {
     require(!out && !stream, "a differentiable call takes neither out nor stream");
@@ -206,6 +219,7 @@ std::pair<Tensor, Tensor> quantise(const Tensor& x, int format, const std::optio
                                    const Stream& stream) {
   const Rows r = rows_of(x, "x");
   require(r.dim >= 1, "rows must have at least one column");
+  check_no_tangent({&x, given(weights), given(codes), given(scales)});
   const int64_t nb = blocks_of(r.dim);
   c10::SmallVector<int64_t, 4> shape(x.sizes().begin(), x.sizes().end() - 1);
   if (weights) {
@@ -271,6 +285,7 @@ void cache_write(const Tensor& x, const Tensor& slots, const Tensor& codes, cons
   const indexer_cache_t cache = cache_of(codes, scales, &x);
   if (r.dim != cache.dim) throw py::value_error(text("x has rows of ", r.dim, " columns, the cache ", cache.dim));
   check_vector(slots, "slots", ScalarType::Int, r.tokens, x);
+  check_no_tangent({&x, &codes, &scales});
   const c10::cuda::CUDAGuard guard(x.device());
   check_status(indexer_cache_write(x.data_ptr(), r.ts, r.dtype, r.tokens, slots.data_ptr<int32_t>(), format, &cache,
                                    stream_of(stream, x)),
@@ -283,6 +298,7 @@ Tensor cache_read(const Tensor& codes, const Tensor& scales, const Tensor& slots
   const indexer_cache_t cache = cache_of(codes, scales, nullptr);
   check_tensor(slots, "slots", ScalarType::Int, &codes);
   require(slots.is_contiguous(), "slots must be contiguous");
+  check_no_tangent({&codes, &scales, given(out)});
   c10::SmallVector<int64_t, 4> shape(slots.sizes().begin(), slots.sizes().end());
   shape.push_back(cache.dim);
   if (out) check_contiguous(*out, "out", kTypes[dtype], shape, codes);
@@ -324,6 +340,7 @@ Tensor scores(const Tensor& q, const Tensor& weights, const Tensor& codes, const
   check_contiguous(seq_lens, "seq_lens", ScalarType::Int, {batch, queries}, q);
   const int64_t shape[2] = {batch * queries, row_len};
   if (out) check_contiguous(*out, "out", ScalarType::Float, shape, q);
+  check_no_tangent({&q, &weights, &codes, &scales, given(out)});
   Tensor y = out ? *out : fresh(shape, ScalarType::Float, q, stream);
   const c10::cuda::CUDAGuard guard(q.device());
   check_status(indexer_scores(static_cast<const uint8_t*>(q.data_ptr()), weights.data_ptr<float>(), &cache,

@@ -156,7 +156,8 @@ def indexer_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor
     start + i with start + len(freqs) + i, "interleaved" pairs 2i with 2i + 1. Angles keep
     their precision at any position. transpose: the rotation of a gradient (by the opposite
     angle, with the same scale). out: a tensor like x, or x itself for a call in place.
-    Differentiable in x (twice too); a call with `out` or `stream` is not."""
+    Differentiable in x by backward (twice too); a call with `out` or `stream` is not, and
+    forward-mode tangents are refused."""
     f = (_binding or _load_binding()).rotary
     how = _choice(layout, _LAYOUTS, "layout")
     if stream is not None:

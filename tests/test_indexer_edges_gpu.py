@@ -202,3 +202,35 @@ def test_topk_output_made_on_another_stream(fw, which):
         assert torch.equal(seen.sort(1).values, want)
     finally:
         fw.topk_set_chip_split(before)
+
+
+# ---------------------------------------------------------------- autograd
+
+def test_forward_mode_is_refused(fw):
+    """No forward derivative is dropped silently."""
+    import torch.autograd.forward_ad as fwd
+    x, v = torch.randn((4, 2, 16), generator=gen(3)).cuda(), torch.ones((4, 2, 16), device="cuda")
+    positions = torch.arange(4, dtype=torch.int32).cuda()
+    freqs, _ = fw.indexer_rotary_freqs(8)
+    codes, scales = make_cache(2, 4, 16)
+    slots = torch.arange(4, dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, v)
+        with pytest.raises(ValueError, match="forward-mode"):
+            fw.indexer_rotary(dual, positions, freqs)
+        with pytest.raises(ValueError, match="forward-mode"):
+            fw.indexer_rotary(dual, positions, freqs, stream=side)
+        with pytest.raises(ValueError, match="forward-mode"):
+            fw.indexer_rotary(x, positions, freqs, out=dual)
+        with pytest.raises(ValueError, match="forward-mode"):
+            fw.indexer_quantise(dual)
+        with pytest.raises(ValueError, match="forward-mode"):
+            fw.indexer_cache_write(dual[:, 0], slots, codes, scales)
+        plain = fw.indexer_rotary(fwd.unpack_dual(dual).primal, positions, freqs)  # without its tangent
+        with torch.no_grad():  # backward is off, forward is not
+            with pytest.raises(ValueError, match="forward-mode"):
+                fw.indexer_rotary(dual, positions, freqs)
+        with torch.inference_mode():  # both are off
+            assert torch.equal(fw.indexer_rotary(dual, positions, freqs), plain)
+    assert torch.equal(fw.indexer_rotary(x, positions, freqs), plain)
