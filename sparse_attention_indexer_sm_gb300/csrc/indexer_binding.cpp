@@ -130,6 +130,11 @@ Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& x, const Stre
   return t;
 }
 
+// A tensor of the caller's that a call has written: autograd is told, for the sake of operations that saved it.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // ---------------------------------------------------------------- rotary positions
 
 void run_rotary(const Tensor& x, const Rows& r, const Tensor& positions, const Tensor& freqs, int layout, int64_t start,
@@ -207,6 +212,7 @@ Tensor rotary(const Tensor& x, const Tensor& positions, const Tensor& freqs, int
     y = fresh(x.sizes(), x.scalar_type(), x, stream);
   }
   run_rotary(x, r, positions, freqs, layout, start, scale, transpose, y, stream);
+  if (out) written(y);
   return y;
 }
 
@@ -238,6 +244,8 @@ std::pair<Tensor, Tensor> quantise(const Tensor& x, int format, const std::optio
                                 static_cast<int32_t>(r.dim), format, weights ? weights->data_ptr<float>() : nullptr,
                                 static_cast<uint8_t*>(c.data_ptr()), s.data_ptr<float>(), stream_of(stream, x)),
                "indexer_quantise");
+  if (codes) written(c);
+  if (scales) written(s);
   return {c, s};
 }
 
@@ -290,6 +298,8 @@ void cache_write(const Tensor& x, const Tensor& slots, const Tensor& codes, cons
   check_status(indexer_cache_write(x.data_ptr(), r.ts, r.dtype, r.tokens, slots.data_ptr<int32_t>(), format, &cache,
                                    stream_of(stream, x)),
                "indexer_cache_write");
+  written(codes);
+  written(scales);
 }
 
 Tensor cache_read(const Tensor& codes, const Tensor& scales, const Tensor& slots, int dtype, const std::optional<Tensor>& out,
@@ -307,6 +317,7 @@ Tensor cache_read(const Tensor& codes, const Tensor& scales, const Tensor& slots
   check_status(indexer_cache_read(&cache, slots.data_ptr<int32_t>(), slots.numel(), dtype, y.data_ptr(),
                                   stream_of(stream, codes)),
                "indexer_cache_read");
+  if (out) written(y);
   return y;
 }
 
@@ -348,6 +359,7 @@ Tensor scores(const Tensor& q, const Tensor& weights, const Tensor& codes, const
                               static_cast<int32_t>(batch), static_cast<int32_t>(queries), static_cast<int32_t>(heads), row_len,
                               y.data_ptr<float>(), stream_of(stream, q)),
                "indexer_scores");
+  if (out) written(y);
   return y;
 }
 

@@ -234,3 +234,41 @@ def test_forward_mode_is_refused(fw):
         with torch.inference_mode():  # both are off
             assert torch.equal(fw.indexer_rotary(dual, positions, freqs), plain)
     assert torch.equal(fw.indexer_rotary(x, positions, freqs), plain)
+
+
+def test_writing_over_a_saved_tensor_is_noticed(fw):
+    """An output that another operation saved for its backward: autograd says that it was changed."""
+    positions = torch.arange(4, dtype=torch.int32).cuda()
+    freqs, _ = fw.indexer_rotary_freqs(8)
+    rows = torch.randn((4, 16), generator=gen(4)).cuda()
+    codes, scales = make_cache(2, 2, 16)
+    slots = torch.arange(4, dtype=torch.int32).cuda()
+    q = torch.zeros((1, 1, 2, 128), device="cuda").to(E4M3)
+    wide = make_cache(2, 2)
+    table, lens = torch.arange(2, dtype=torch.int32).cuda()[None], torch.full((1, 1), 4, dtype=torch.int32).cuda()
+    held = torch.zeros((4, 1), device="cuda")
+    spare = torch.empty((4, 16), device="cuda").to(E4M3)
+    calls = [
+        ((4, 16), lambda t: fw.indexer_rotary(rows, positions, freqs, out=t)),
+        ((4, 16), lambda t: fw.indexer_rotary(t, positions, freqs, out=t)),
+        ((4, 16), lambda t: fw.indexer_rotary(rows, positions, freqs, out=t, stream=torch.cuda.current_stream())),
+        ((4, 1), lambda t: fw.indexer_quantise(rows, codes=spare, scales=t)),
+        ((2, 2, 1), lambda t: fw.indexer_cache_write(rows, slots, codes, t)),
+        ((4, 16), lambda t: fw.indexer_cache_read(codes, scales, slots, dtype=torch.float32, out=t)),
+        ((1, 4), lambda t: fw.indexer_scores(q, torch.ones((1, 1, 2), device="cuda"), *wide, table, lens, 4, out=t)),
+    ]
+    for shape, write in calls:
+        saved = torch.ones(shape, device="cuda")
+        leaf = torch.ones(shape, device="cuda", requires_grad=True)
+        y = (leaf * saved).sum()
+        write(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    for t, write in ((spare, lambda: fw.indexer_quantise(rows, codes=spare, scales=held)),
+                     (codes, lambda: fw.indexer_cache_write(rows, slots, codes, scales))):
+        before = t._version
+        write()
+        assert t._version == before + 1
+    with torch.inference_mode():
+        out = torch.empty((4, 16), device="cuda")
+    assert fw.indexer_rotary(rows, positions, freqs, out=out) is out  # an inference tensor has no version
