@@ -176,7 +176,8 @@ def indexer_quantise(x: torch.Tensor, *, scale_format: str = "fp32",
     scale_format: "fp32" (amax / 448) or "pow2" (the next power of two). weights: fp32
     [tokens, heads] (or [tokens]), for rows of one block: scales then holds
     weights * scale, of the same shape, as indexer_scores takes it. A block that holds an
-    infinity or a NaN becomes NaN throughout. codes, scales: contiguous outputs."""
+    infinity or a NaN becomes NaN throughout. codes, scales: contiguous outputs. There is no
+    gradient: tensors that require one are refused while gradients are recorded."""
     f = (_binding or _load_binding()).quantise
     fmt = _choice(scale_format, _FORMATS, "scale_format")
     if stream is not None:
@@ -190,7 +191,8 @@ def indexer_cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tenso
     slots[t] = page * page_size + offset of a cache: codes [pages, page_size, dim]
     float8_e4m3fn, scales [pages, page_size, ceil(dim / 128)] fp32 (views of one buffer are
     fine). Slot -1: the row is not written. Another slot outside the cache is not written
-    either, and counted (indexer_guard_hits). Slots should differ from each other."""
+    either, and counted (indexer_guard_hits). Slots should differ from each other. There is
+    no gradient, as in indexer_quantise."""
     f = (_binding or _load_binding()).cache_write
     fmt = _choice(scale_format, _FORMATS, "scale_format")
     if stream is not None:
@@ -204,7 +206,8 @@ def indexer_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.T
                        stream=None) -> torch.Tensor:
     """The cache rows at `slots` (int32, contiguous, any shape; the positions that
     topk_transform_paged writes are such slots) as `dtype`: [*slots.shape, dim]. Slot -1
-    gives zeros; another slot outside the cache too, and is counted (indexer_guard_hits)."""
+    gives zeros; another slot outside the cache too, and is counted (indexer_guard_hits).
+    There is no gradient, as in indexer_quantise."""
     f = (_binding or _load_binding()).cache_read
     kind = _choice(dtype, _DTYPES, "dtype")
     if stream is not None:
@@ -227,7 +230,8 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, 
     (indexer_quantise with weights), both contiguous; the cache's codes
     [pages, page_size, 128] and scales [pages, page_size, 1]; page_table int32 [batch, P]
     with P * page_size >= row_len; seq_lens int32 [batch, queries]. Positions on a page
-    outside the cache get -inf and are counted (indexer_guard_hits)."""
+    outside the cache get -inf and are counted (indexer_guard_hits). There is no gradient, as
+    in indexer_quantise."""
     f = (_binding or _load_binding()).scores
     if stream is not None:
         return _on(stream, f, q, weights, codes, scales, page_table, seq_lens, row_len, out)

@@ -272,3 +272,36 @@ def test_writing_over_a_saved_tensor_is_noticed(fw):
     with torch.inference_mode():
         out = torch.empty((4, 16), device="cuda")
     assert fw.indexer_rotary(rows, positions, freqs, out=out) is out  # an inference tensor has no version
+
+
+def test_gradients_that_do_not_exist_are_refused(fw):
+    """The 8-bit operators have no gradient: an input that asks for one is not detached silently."""
+    rows = torch.randn((4, 2, 128), generator=gen(5)).cuda()
+    w = torch.ones((4, 2), device="cuda")
+    codes, scales = make_cache(2, 4)
+    slots = torch.arange(4, dtype=torch.int32).cuda()
+    q8, w8 = fw.indexer_quantise(rows, weights=w)
+    table, lens = torch.arange(2, dtype=torch.int32).cuda()[None], torch.full((1, 4), 8, dtype=torch.int32).cuda()
+
+    def scores(weights=w8, s=scales, out=None):
+        return fw.indexer_scores(q8[None], weights[None], codes, s, table, lens, 8, out=out)
+
+    def leaf(t):
+        return t.clone().requires_grad_(True)
+
+    calls = [lambda: fw.indexer_quantise(leaf(rows)), lambda: fw.indexer_quantise(rows, weights=leaf(w)),
+             lambda: fw.indexer_quantise(rows, weights=w, scales=leaf(w)),
+             lambda: fw.indexer_cache_write(leaf(rows)[:, 0], slots, codes, scales),
+             lambda: fw.indexer_cache_write(rows[:, 0], slots, codes, leaf(scales)),
+             lambda: fw.indexer_cache_read(codes, leaf(scales), slots),
+             lambda: fw.indexer_cache_read(codes, scales, slots, dtype=torch.float32,
+                                           out=leaf(torch.zeros((4, 128), device="cuda"))),
+             lambda: scores(weights=leaf(w8)), lambda: scores(s=leaf(scales)),
+             lambda: scores(out=leaf(torch.zeros((4, 8), device="cuda")))]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert torch.equal(scores(weights=leaf(w8).detach()), scores())
