@@ -77,9 +77,11 @@ static_assert(kMaxSpanSlices * 4 <= kKeyStages * kTile * kDim, "their sums fit t
 constexpr int kWaitLimit = 1 << 17;      // tries of a wait before it is given up,
 constexpr uint32_t kWaitNs = 20000;      // each of which may sleep this long: 2.6 s in all
 
-// A scale that stands for a page outside the cache; NaN scales of the cache get other bits.
+// A scale that stands for a page outside the cache; every NaN scale of the cache gets other bits as it is read.
 constexpr uint32_t kNoPage = 0x7fc00001u;
 constexpr uint32_t kNan = 0x7fffffffu;
+
+__device__ __forceinline__ uint32_t scale_bits(uint32_t v) { return (v & 0x7fffffffu) > 0x7f800000u ? kNan : v; }
 
 // Pages outside the cache that were met, and waits that ran out (see indexer_guard_hits).
 __device__ unsigned int g_guard_hits;
@@ -685,14 +687,14 @@ __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, in
             for (int q = 0; q < 4; ++q) got[u][q] = kNoPage;
             if (inside && p.quads == 2) {
               const uint4 v = *reinterpret_cast<const uint4*>(src);
-              got[u][0] = v.x, got[u][1] = v.y, got[u][2] = v.z, got[u][3] = v.w;
+              got[u][0] = scale_bits(v.x), got[u][1] = scale_bits(v.y), got[u][2] = scale_bits(v.z), got[u][3] = scale_bits(v.w);
             } else if (inside) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) got[u][q] = __float_as_uint(src[q * p.scale_ts]);
+              for (int q = 0; q < 4; ++q) got[u][q] = scale_bits(__float_as_uint(src[q * p.scale_ts]));
             }
           } else {
             got[u][k] = kNoPage;
-            if (inside) got[u][k] = __float_as_uint(*src);
+            if (inside) got[u][k] = scale_bits(__float_as_uint(*src));
           }
           if (!inside && off[u][k] != 0xffffffffu) atomicAdd(&g_guard_hits, 1u);
         }
@@ -701,11 +703,6 @@ __device__ __forceinline__ void load_scales(const ScoresParams& p, Shared& s, in
       for (int u = 0; u < kScaleBatch; ++u) {
         const int tile = t + u * step;
         if (tile >= it.seen) break;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t v = got[u][q];
-          got[u][q] = (v & 0x7fffffffu) > 0x7f800000u && v != kNoPage ? kNan : v;
-        }
         const uint32_t unit = (tiles + (tile - it.first)) * p.units + (p.units == 1 ? 0 : turn & 1);
         const uint32_t at = unit & ((1u << p.tmem_shift) - 1);
         bar_pass(s, smem_addr(&s.tmem_empty[at]), (unit >> p.tmem_shift & 1u) ^ 1u);

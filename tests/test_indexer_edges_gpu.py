@@ -3,6 +3,8 @@ other streams work, and what autograd and the allocator are owed."""
 
 from __future__ import annotations
 
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -305,3 +307,25 @@ def test_gradients_that_do_not_exist_are_refused(fw):
         for call in calls:
             call()
     assert torch.equal(scores(weights=leaf(w8).detach()), scores())
+
+
+# ---------------------------------------------------------------- scores
+
+@pytest.mark.parametrize("page_size,strided", [(64, False), (64, True), (3, False), (1, False)])
+def test_every_nan_scale_makes_its_scores_nan(fw, page_size, strided):
+    """Every bit pattern of a NaN, those that a kernel might use as a mark among them."""
+    n = 24
+    pages = -(-n // page_size)
+    patterns = [0x7fc00000, 0x7fc00001, 0x7f800001, 0x7fffffff, -1, -0x400000, -0x3fffff, 0x7fc00002]
+    codes = torch.full((pages, page_size, 128), 1.0, device="cuda").to(E4M3)
+    bits = torch.full((pages, page_size, 2 if strided else 1), 0x3f800000, dtype=torch.int32, device="cuda")
+    for i, v in enumerate(patterns):
+        j = 3 * i
+        bits[j // page_size, j % page_size] = v
+    scales = bits.view(torch.float32)[..., :1]
+    q, w = torch.ones((1, 1, 4, 128), device="cuda").to(E4M3), torch.ones((1, 1, 4), device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    got = fw.indexer_scores(q, w, codes, scales, table, torch.full((1, 1), n, dtype=torch.int32, device="cuda"), n)
+    want = torch.full((1, n), 512.0)
+    want[0, ::3] = math.nan
+    assert torch.equal(got.cpu().nan_to_num(-1.0), want.nan_to_num(-1.0))
