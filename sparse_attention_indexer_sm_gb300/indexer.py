@@ -40,6 +40,7 @@ INDEXER_MAX_HEADS = 128
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_RAMPS = {"turns": 0, "pairs": 1}
 _FORMATS = {"fp32": 0, "pow2": 1}
 
 _binding = None
@@ -113,7 +114,8 @@ def _on(stream, call, *args):
 
 def indexer_rotary_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None,
                          factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0,
-                         beta_slow: float = 1.0, device="cuda") -> tuple[torch.Tensor, float]:
+                         beta_slow: float = 1.0, ramp: str = "turns",
+                         device="cuda") -> tuple[torch.Tensor, float]:
     """(freqs, scale) for indexer_rotary: fp64 radians per position of the rot_dim / 2
     pairs, base ** (-2 i / rot_dim), and the factor of sine and cosine.
 
@@ -121,7 +123,13 @@ def indexer_rotary_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | 
     frequencies divided by factor); "ntk" (a larger base: the slowest pair divided by
     factor, the fastest kept); "yarn" (pairs that turn more than beta_fast times within
     original_len kept, those that turn less than beta_slow times divided by factor, those
-    between blended; scale = 0.1 ln(factor) + 1)."""
+    between blended; scale = 0.1 ln(factor) + 1).
+
+    ramp, how yarn blends: "turns", linearly in the number of turns; or "pairs", linearly in
+    the pair's index between the pairs that turn beta_fast times (rounded down) and beta_slow
+    times (rounded up), as the method's published code does and the checkpoints trained with
+    it expect: take the one that the model was trained with. A model that puts the factor
+    into its softmax ignores `scale`."""
     if rot_dim < 2 or rot_dim % 2 != 0:
         raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
     if not base > 1.0 or not factor >= 1.0:
@@ -135,8 +143,14 @@ def indexer_rotary_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | 
     elif scaling == "yarn":
         if not beta_fast > beta_slow:
             raise ValueError("beta_fast must be above beta_slow")
-        turns = original_len * freqs / (2.0 * math.pi)
-        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        if _choice(ramp, _RAMPS, "ramp") == 0:
+            turns = original_len * freqs / (2.0 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        else:
+            low, high = (rot_dim * math.log(original_len / (2.0 * math.pi * b)) / (2.0 * math.log(base))
+                         for b in (beta_fast, beta_slow))
+            low, high = max(math.floor(low), 0), min(math.ceil(high), rot_dim - 1)
+            keep = 1.0 - ((i - low) / max(high - low, 1)).clamp(0.0, 1.0)
         freqs = freqs * keep + freqs / factor * (1.0 - keep)
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
