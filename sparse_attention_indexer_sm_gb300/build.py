@@ -3,12 +3,14 @@
 Every object is compiled for sm_103a only, all of them in parallel, then linked
 against the shared CUDA runtime (so that the process keeps a single runtime
 together with PyTorch). Beside it stands the indexer operators' Python binding, a
-C++ module for this interpreter and this PyTorch, linked against the library. Run
-``python -m sparse_attention_indexer_sm_gb300.build``.
+C++ module for this interpreter and this PyTorch, linked against the library, which
+does not depend on it: a binding that cannot be built leaves the library in place.
+Run ``python -m sparse_attention_indexer_sm_gb300.build``.
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -44,14 +46,19 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
+def _pytorch() -> bool:
+    """Whether there is a PyTorch to build the binding for."""
+    return importlib.util.find_spec("torch") is not None
+
+
 def binding_path() -> str:
-    """The binding's module, of this PyTorch's version."""
+    """The binding's module, of this interpreter's and this PyTorch's version."""
     import torch
-    return os.path.join(BUILD_DIR, f"indexer_binding-{torch.__version__}.so")
+    return os.path.join(BUILD_DIR, f"indexer_binding-{sys.implementation.cache_tag}-{torch.__version__}.so")
 
 
 def _stale() -> bool:
-    outs = [LIB_PATH, binding_path()]
+    outs = [LIB_PATH, binding_path()] if _pytorch() else [LIB_PATH]
     if not all(os.path.exists(p) for p in outs):
         return True
     t = min(os.path.getmtime(p) for p in outs)
@@ -103,24 +110,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         start(cmd)
         objs.append(obj)
-    binding = binding_path()
-    binding_tmp = binding + f".{os.getpid()}.tmp"
-    compile_binding, link_binding = _binding_commands(os.path.join(BUILD_DIR, "indexer_binding.o"), binding_tmp,
-                                                      cuda_home)
-    start(compile_binding)
-    for cmd, p in procs:
+    without_compiler = None
+    if _pytorch():
+        binding = binding_path()
+        binding_tmp = binding + f".{os.getpid()}.tmp"
+        compile_binding, link_binding = _binding_commands(os.path.join(BUILD_DIR, "indexer_binding.o"), binding_tmp,
+                                                          cuda_home)
+        try:
+            start(compile_binding)
+        except OSError as e:  # raised again once the library stands
+            without_compiler = e
+
+    def finish(cmd, p):
         out, _ = p.communicate()
         if p.returncode != 0:
             raise RuntimeError(f"compiler failed ({' '.join(cmd)}):\n{out}")
         if verbose and out:
             print(out, file=sys.stderr)
+
+    for cmd, p in procs[:len(objs)]:
+        finish(cmd, p)
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cuda_lib = os.path.join(cuda_home, "lib64")
     _run([exe, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + cuda_lib,
           "-Xlinker", "-soname,libtopk_transform.so", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB_PATH)
-    _run(link_binding, "link of the binding")
-    os.replace(binding_tmp, binding)
+    if without_compiler is not None:
+        raise RuntimeError(f"compiler failed ({' '.join(compile_binding)}): {without_compiler}")
+    if _pytorch():
+        finish(*procs[-1])
+        _run(link_binding, "link of the binding")
+        os.replace(binding_tmp, binding)
     return LIB_PATH
 
 

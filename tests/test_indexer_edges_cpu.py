@@ -1,6 +1,8 @@
 """The indexer's operators at the edges of their contracts, without a GPU."""
 
 import math
+import os
+import sys
 
 import pytest
 
@@ -55,3 +57,35 @@ def test_yarn_ramps():
     assert math.isclose((turns / plain)[16].item(), share + (1 - share) / 40, rel_tol=1e-12)
     with pytest.raises(ValueError, match="ramp"):
         fw.indexer_rotary_freqs(64, ramp="other", **kw)
+
+
+# ---------------------------------------------------------------- build
+
+@pytest.mark.parametrize("compiler", ["false", "no-such-compiler"])
+def test_library_stands_without_the_binding(compiler, tmp_path, monkeypatch):
+    """A binding that does not compile ends the build with an error, but after the library is linked."""
+    from sparse_attention_indexer_sm_gb300 import build
+    stub = tmp_path / "bin" / "nvcc"  # writes the file that follows -o
+    stub.parent.mkdir()
+    stub.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\necho "$@" > "$2"\n')
+    stub.chmod(0o755)
+    out = tmp_path / "_build"
+    monkeypatch.setattr(build, "BUILD_DIR", str(out))
+    monkeypatch.setattr(build, "LIB_PATH", str(out / "libtopk_transform.so"))
+    monkeypatch.setattr(build, "nvcc", lambda: str(stub))
+    monkeypatch.setenv("CXX", compiler)
+    with pytest.raises(RuntimeError, match="compiler failed"):
+        build.build()
+    assert (out / "libtopk_transform.so").exists() and not os.path.exists(build.binding_path())
+    with monkeypatch.context() as m:  # no PyTorch: the library alone
+        m.setattr(build, "_pytorch", lambda: False)
+        m.delattr(build, "binding_path")
+        assert build.build(force=True) == build.build() == build.LIB_PATH
+    monkeypatch.setenv("CXX", str(stub))
+    assert build.build() == build.LIB_PATH and os.path.exists(build.binding_path())
+
+
+def test_binding_belongs_to_its_interpreter_and_pytorch():
+    from sparse_attention_indexer_sm_gb300 import build
+    name = os.path.basename(build.binding_path())
+    assert sys.implementation.cache_tag in name and torch.__version__ in name
