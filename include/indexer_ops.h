@@ -139,10 +139,15 @@ int indexer_scores(const uint8_t* q, const float* weights, const indexer_cache_t
                    cudaStream_t stream);
 
 /* Slots and page ids outside the cache met on the current device since the last reset
- * (each at least once), and kernels' waits that ran out (never, unless there is a bug).
- * Both wait for the device's pending work. */
+ * (each at least once), and kernels' waits that ran out (never, unless there is a bug: the
+ * scores concerned are NaN then). Both wait for all of the device's pending work. */
 int indexer_guard_hits(uint64_t* hits);
 int indexer_reset_guard_hits(void);
+
+/* For tests (process-wide; returns the previous value): later calls of indexer_scores act as
+ * if a wait of every CTA had run out (1) or its shared memory were not aligned (2): scores
+ * are NaN, and are counted in indexer_guard_hits. Anything else: 0, no failure. */
+int indexer_set_scores_failure(int mode);
 
 #ifdef __cplusplus
 }

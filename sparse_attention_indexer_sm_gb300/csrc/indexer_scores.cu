@@ -101,6 +101,7 @@ struct ScoresParams {
   int32_t tiles, chunk;            // tiles of a row; tiles of an item
   int32_t tmem_shift, tmem_stride; // 2^tmem_shift stages of tmem_stride columns
   int32_t units, unit_queries;     // units of a tile (1 or 2); queries of a unit
+  int32_t fail;                    // for tests: 1 as if a wait had run out, 2 as if shared memory were misaligned
 };
 
 struct Shared {
@@ -185,7 +186,7 @@ __device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity) {
 }
 
 // A wait of the other roles, which go on in any case: after a wait that ran out they run through to their end
-// with wrong numbers (and the count in g_guard_hits), in bounds.
+// with wrong numbers, in bounds, over which the epilogue then writes NaN (and the count is in g_guard_hits).
 __device__ __forceinline__ void bar_pass(Shared& s, uint32_t addr, uint32_t parity) {
   bar_wait_thread(s, addr, parity);
   __syncwarp();
@@ -875,6 +876,29 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
   }
 }
 
+// After a wait that ran out (rarely run, so out of line): NaN in place of every score that this epilogue warp has written. What is wrong among them was
+// read after the wait's end was noted.
+template <int kGroups, bool kSpans>
+__device__ __noinline__ void give_up(const ScoresParams& p, const Shared& s, int head_rows, int wg) {
+  const int tid = threadIdx.x & 127, queries = Plan<kGroups>::kColumns / head_rows;
+  const int first = kGroups == 4 || p.units == 2 ? wg * queries : 0;
+  uint32_t tiles = 0;
+  if (p.fail != 0 && tid == 0) atomicAdd(&g_guard_hits, 1u);
+  for (Walk<kSpans> walk(s); walk.more(p); walk.on()) {
+    Item it = item_at(p, walk, 0);
+    item_ready(p, walk, it);
+    const int64_t query = it.query + first;
+    for (int g = 0; g < min(it.count - first, queries); ++g) {
+      const int32_t len = clamped(p, p.seq_lens[query + g]);
+      for (int t = first_tile<kGroups>(p, it, wg, tiles); t < it.seen; t += tile_step<kGroups>(p)) {
+        const int32_t j = t * kTile + tid;
+        if (j < len) p.out[(query + g) * p.row_len + j] = __uint_as_float(kNan);
+      }
+    }
+    tiles += it.seen - it.first;
+  }
+}
+
 template <int kRegisters>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
@@ -884,14 +908,23 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
 }
 
+// NaN in place of every score of a launch that cannot start (out of line too).
+__device__ __noinline__ void spoil(const ScoresParams& p) {
+  begin_after_prior_grids();
+  const int64_t all = p.slices / p.groups * p.queries * p.row_len, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step)
+    p.out[i] = __uint_as_float(kNan);
+}
+
 // Whether the dynamic shared memory starts where its declared alignment says, which the swizzled tiles rely on. Without a
 // rounding of its address every place in it is a constant, and the registers that held addresses are the epilogue's
-// (2048 queries over 32768 keys, 64 heads: 548 -> 512 us).
-__device__ __forceinline__ bool aligned_base(const Shared& s) {
+// (2048 queries over 32768 keys, 64 heads: 548 -> 512 us). If it ever starts elsewhere, all scores are NaN, and counted.
+__device__ __forceinline__ bool aligned_base(const ScoresParams& p, const Shared& s) {
   uint32_t base = smem_addr(&s);
   asm volatile("" : "+r"(base));
-  if (base % 1024 == 0) return true;
+  if (__builtin_expect(base % 1024 == 0 && p.fail != 2, 1)) return true;
   if (threadIdx.x == 0) atomicAdd(&g_guard_hits, 1u);
+  spoil(p);
   return false;
 }
 
@@ -899,12 +932,12 @@ __device__ __forceinline__ bool aligned_base(const Shared& s) {
 // tensor map's heads) and their weights are 0.
 template <int kGroups, bool kSpans, int kHeads>
 __global__ void __launch_bounds__(kThreads<kGroups>, 1)
-    scores_kernel(const ScoresParams p, const __grid_constant__ CUtensorMap key_map,
+    scores_kernel(const __grid_constant__ ScoresParams p, const __grid_constant__ CUtensorMap key_map,
                   const __grid_constant__ CUtensorMap query_map) {
   using P = Plan<kGroups>;
   extern __shared__ __align__(1024) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
-  if (!aligned_base(s)) return;
+  if (!aligned_base(p, s)) return;
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&key_map) : "memory");
@@ -922,7 +955,7 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
       bar_init(&s.tmem_empty[i], kGroups == 2 ? 4 : 16);  // the warps that read it
     }
     bar_init(&s.drained, P::kMultipliers);
-    s.aborted = 0;
+    s.aborted = p.fail;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -958,6 +991,8 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
     if constexpr (kSpans)  // while the first tiles are on their way
       fill_rest(p, static_cast<int64_t>(warp - kFirstWarp<kGroups>) * gridDim.x + blockIdx.x, 4 * kGroups * static_cast<int64_t>(gridDim.x));
     reduce<kGroups, kSpans, kHeads>(p, s, tmem, (warp - kFirstWarp<kGroups>) / 4);
+    if (__builtin_expect(*const_cast<volatile int32_t*>(&s.aborted) != 0, 0))
+      give_up<kGroups, kSpans>(p, s, kHeads, (warp - kFirstWarp<kGroups>) / 4);
   }
 
   tmem_fence_before();
@@ -968,6 +1003,8 @@ __global__ void __launch_bounds__(kThreads<kGroups>, 1)
 }
 
 constexpr size_t kSmemBytes = sizeof(Shared);
+
+std::atomic<int> g_fail{0};
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1078,6 +1115,7 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
             : p.scale_ts == 1 && p.scale_ps % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0 ? 2 : 1;
   p.queries = queries;
   p.heads = heads;
+  p.fail = g_fail.load(std::memory_order_relaxed);
   const int head_rows = heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
   p.group = kMaxColumns / head_rows < queries ? kMaxColumns / head_rows : queries;
   p.groups = (queries + p.group - 1) / p.group;
@@ -1139,4 +1177,8 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
                           : run(plan, integral_constant<int, 128>());
   }
   return status_of(e);
+}
+
+extern "C" int indexer_set_scores_failure(int mode) {
+  return indexer_gb300::g_fail.exchange(mode == 1 || mode == 2 ? mode : 0, std::memory_order_relaxed);
 }

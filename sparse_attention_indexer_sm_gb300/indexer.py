@@ -84,6 +84,7 @@ def declare(lib: ctypes.CDLL) -> None:
         "indexer_scores": [vp, vp, vp, vp, i64, vp, i32, i32, i32, i64, vp, vp],
         "indexer_guard_hits": [ctypes.POINTER(ctypes.c_uint64)],
         "indexer_reset_guard_hits": [],
+        "indexer_set_scores_failure": [i32],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

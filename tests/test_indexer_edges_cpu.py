@@ -89,3 +89,11 @@ def test_binding_belongs_to_its_interpreter_and_pytorch():
     from sparse_attention_indexer_sm_gb300 import build
     name = os.path.basename(build.binding_path())
     assert sys.implementation.cache_tag in name and torch.__version__ in name
+
+
+def test_failure_mode_of_scores():
+    from sparse_attention_indexer_sm_gb300 import build
+    build.build()
+    import sparse_attention_indexer_sm_gb300 as fw
+    lib = fw.load_library()
+    assert [lib.indexer_set_scores_failure(m) for m in (1, 2, 3, 0)] == [0, 1, 2, 0]

@@ -329,3 +329,43 @@ def test_every_nan_scale_makes_its_scores_nan(fw, page_size, strided):
     want = torch.full((1, n), 512.0)
     want[0, ::3] = math.nan
     assert torch.equal(got.cpu().nan_to_num(-1.0), want.nan_to_num(-1.0))
+
+
+def scores_inputs(seed, b, n, h, row_len, page_size, lens=None):
+    g = gen(seed)
+    pages = -(-row_len // page_size)
+    codes = (torch.randn((b * pages, page_size, 128), generator=g) * 90).clamp(-448, 448).to(E4M3).cuda()
+    scales = (torch.rand((b * pages, page_size, 1), generator=g) * 0.02 + 0.001).cuda()
+    table = torch.randperm(b * pages, generator=g).view(b, pages).int().cuda()
+    q = (torch.randn((b, n, h, 128), generator=g) * 90).clamp(-448, 448).to(E4M3).cuda()
+    w = torch.randn((b, n, h), generator=g).cuda()
+    if lens is None:
+        lens = torch.randint(0, row_len + 1, (b, n), generator=g).int()
+    return q, w, codes, scales, table, lens.cuda(), row_len
+
+
+@pytest.mark.parametrize("case", [(3, 1, 64, 1000, 64), (2, 2, 128, 600, 64), (5, 4, 64, 700, 48), (2, 33, 16, 500, 1),
+                                  (200, 1, 64, 6000, 64), (40, 5, 32, 24000, 64)])
+def test_a_call_that_gives_up_has_no_wrong_scores(fw, case):
+    """What was computed around a wait that ran out is NaN, and so is everything where the kernel cannot start;
+    both are counted. Later calls are as before."""
+    lib = fw.load_library()
+    args = scores_inputs(sum(case), *case)
+    want = fw.indexer_scores(*args)
+    seen = torch.arange(case[3], device="cuda") < args[5].view(-1, 1)
+    for mode in (1, 2):
+        out = torch.zeros_like(want)
+        assert lib.indexer_set_scores_failure(mode) == 0
+        try:
+            fw.indexer_scores(*args, out=out)
+            torch.cuda.synchronize()
+        finally:
+            assert lib.indexer_set_scores_failure(0) == mode
+        assert fw.indexer_guard_hits() > 0
+        fw.indexer_reset_guard_hits()
+        assert bool(torch.isnan(out[seen]).all())
+        if mode == 1:
+            assert bool((out[~seen] == -math.inf).all())
+        else:
+            assert bool(torch.isnan(out).all())
+        assert torch.equal(fw.indexer_scores(*args), want)
