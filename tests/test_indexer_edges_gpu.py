@@ -369,3 +369,45 @@ def test_a_call_that_gives_up_has_no_wrong_scores(fw, case):
         else:
             assert bool(torch.isnan(out).all())
         assert torch.equal(fw.indexer_scores(*args), want)
+
+
+KEY_TILE, ITEM_COST, MOST_SLICES = 128, 4, 8192  # csrc/indexer_scores.cu: kTile, kItemCost, kMaxSpanSlices
+
+
+def in_spans(b, n, h, row_len):
+    """Whether CTAs of a call share its tiles out by the rows' lengths, or take items in turn."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    columns = next(c for c in (16, 32, 64, 128) if h <= c)
+    slices, tiles = b * -(-n // min(256 // columns, n)), -(-row_len // KEY_TILE)
+    return (slices <= MOST_SLICES and slices * (tiles + ITEM_COST) < 2**31 and slices * tiles >= sms * (32 + slices // 64))
+
+
+@pytest.mark.parametrize("n,h,row_len,page_size", [
+    (1, 64, 12000, 64), (1, 64, 12001, 1), (1, 64, 11999, 3), (16, 16, 12000, 64), (16, 16, 9000, 1), (4, 64, 9001, 1),
+    (4, 64, 9000, 3), (3, 128, 6000, 20), (3, 128, 6001, 1), (8, 32, 9000, 48), (9, 24, 9000, 1), (5, 64, 7000, 128)])
+def test_spans_against_items_in_turn(fw, n, h, row_len, page_size):
+    """As many sequences as it takes for spans, of every mix of lengths: the same bits as each sequence by itself,
+    in items in turn, and some rows against 64 bits."""
+    from test_indexer_gpu import check_scores
+    b = next(b for b in range(1, MOST_SLICES) if in_spans(b, n, h, row_len)) * 9 // 8 + 1
+    assert in_spans(b, n, h, row_len) and not in_spans(1, n, h, row_len)
+    g = gen(n + h + page_size)
+    q, w, codes, scales, table, _, _ = scores_inputs(n * h + page_size, b, n, h, row_len, page_size)
+    short = (torch.rand((b, n), generator=g) ** 4 * row_len).int()
+    mixed = torch.where(torch.rand((b, 1), generator=g) < 0.2, row_len, short).int()
+    mixed[::7] = 0
+    last = torch.zeros((b, n), dtype=torch.int32)
+    last[-1, -1] = row_len - 3
+    steps = (row_len - n + 1 + torch.arange(n, dtype=torch.int32)).expand(b, n).contiguous()
+    for lens in (mixed, torch.zeros((b, n), dtype=torch.int32), last, steps):
+        lens = lens.cuda()
+        got = fw.indexer_scores(q, w, codes, scales, table, lens, row_len)
+        seen = torch.arange(row_len, device="cuda") < lens.view(-1, 1)
+        assert torch.equal(got == -math.inf, ~seen)
+        for i in range(b):
+            few = fw.indexer_scores(q[i:i + 1], w[i:i + 1], codes, scales, table[i:i + 1], lens[i:i + 1], row_len)
+            assert torch.equal(got[i * n:(i + 1) * n], few), i
+        for i in {0, b // 2, b - 1}:
+            k = i % n  # one query of the sequence
+            check_scores(got[i * n + k:i * n + k + 1], q[i:i + 1, k:k + 1], w[i:i + 1, k:k + 1], codes, scales,
+                         table[i:i + 1], lens[i:i + 1, k:k + 1], row_len)
