@@ -79,21 +79,17 @@ void check_vector(const Tensor& t, const char* name, ScalarType type, int64_t n,
     throw py::value_error(text(name, " must be a contiguous vector of length ", n));
 }
 
-// No operator has a forward-mode derivative: a tangent is refused, not dropped.
-void check_no_tangent(std::initializer_list<const Tensor*> tensors) {
-  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
-  for (const Tensor* t : tensors)
-    if (t != nullptr && t->_fw_grad(/*level=*/0).defined())
+// No operator has a forward-mode derivative: a tangent is refused, not dropped. Nor, `backward` says, has this one a
+// backward: an input that asks for a gradient is refused, not detached. Most tensors carry nothing that could say either,
+// and are done with after one look: the others' questions would cost each call 0.1 to 0.3 us.
+void check_autograd(std::initializer_list<const Tensor*> tensors, bool backward) {
+  for (const Tensor* t : tensors) {
+    if (t == nullptr || t->unsafeGetTensorImpl()->autograd_meta() == nullptr) continue;
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t->_fw_grad(/*level=*/0).defined())
       throw py::value_error("no forward-mode derivative: a tensor of the call carries a tangent");
-}
-
-// The 8-bit operators have no backward either: an input that asks for a gradient is refused, not detached.
-void check_no_gradient(std::initializer_list<const Tensor*> tensors) {
-  check_no_tangent(tensors);
-  if (!at::GradMode::is_enabled()) return;
-  for (const Tensor* t : tensors)
-    if (t != nullptr && t->requires_grad())
+    if (!backward && t->requires_grad() && at::GradMode::is_enabled())
       throw py::value_error("no gradient: a tensor of the call requires one (detach it, or call under torch.no_grad())");
+  }
 }
 
 const Tensor* given(const std::optional<Tensor>& t) { return t ? &*t : nullptr; }
@@ -201,7 +197,7 @@ Tensor rotary(const Tensor& x, const Tensor& positions, const Tensor& freqs, int
           "freqs must be a contiguous fp64 vector of at least one frequency");
   if (start < 0 || start > r.dim || 2 * freqs.size(0) > r.dim - start)
     throw py::value_error(text("columns [", start, ", ", start + 2 * freqs.size(0), ") do not lie within the row of ", r.dim));
-  check_no_tangent({&x, given(out)});
+  check_autograd({&x, given(out)}, true);
   const bool recording = at::GradMode::is_enabled();
   if (recording && x.requires_grad()) {
     require(!out && !stream, "a differentiable call takes neither out nor stream");
@@ -234,7 +230,7 @@ std::pair<Tensor, Tensor> quantise(const Tensor& x, int format, const std::optio
                                    const Stream& stream) {
   const Rows r = rows_of(x, "x");
   require(r.dim >= 1, "rows must have at least one column");
-  check_no_gradient({&x, given(weights), given(codes), given(scales)});
+  check_autograd({&x, given(weights), given(codes), given(scales)}, false);
   const int64_t nb = blocks_of(r.dim);
   c10::SmallVector<int64_t, 4> shape(x.sizes().begin(), x.sizes().end() - 1);
   if (weights) {
@@ -302,7 +298,7 @@ void cache_write(const Tensor& x, const Tensor& slots, const Tensor& codes, cons
   const indexer_cache_t cache = cache_of(codes, scales, &x);
   if (r.dim != cache.dim) throw py::value_error(text("x has rows of ", r.dim, " columns, the cache ", cache.dim));
   check_vector(slots, "slots", ScalarType::Int, r.tokens, x);
-  check_no_gradient({&x, &codes, &scales});
+  check_autograd({&x, &codes, &scales}, false);
   const c10::cuda::CUDAGuard guard(x.device());
   check_status(indexer_cache_write(x.data_ptr(), r.ts, r.dtype, r.tokens, slots.data_ptr<int32_t>(), format, &cache,
                                    stream_of(stream, x)),
@@ -317,7 +313,7 @@ Tensor cache_read(const Tensor& codes, const Tensor& scales, const Tensor& slots
   const indexer_cache_t cache = cache_of(codes, scales, nullptr);
   check_tensor(slots, "slots", ScalarType::Int, &codes);
   require(slots.is_contiguous(), "slots must be contiguous");
-  check_no_gradient({&codes, &scales, given(out)});
+  check_autograd({&codes, &scales, given(out)}, false);
   c10::SmallVector<int64_t, 4> shape(slots.sizes().begin(), slots.sizes().end());
   shape.push_back(cache.dim);
   if (out) check_contiguous(*out, "out", kTypes[dtype], shape, codes);
@@ -360,7 +356,7 @@ Tensor scores(const Tensor& q, const Tensor& weights, const Tensor& codes, const
   check_contiguous(seq_lens, "seq_lens", ScalarType::Int, {batch, queries}, q);
   const int64_t shape[2] = {batch * queries, row_len};
   if (out) check_contiguous(*out, "out", ScalarType::Float, shape, q);
-  check_no_gradient({&q, &weights, &codes, &scales, given(out)});
+  check_autograd({&q, &weights, &codes, &scales, given(out)}, false);
   Tensor y = out ? *out : fresh(shape, ScalarType::Float, q, stream);
   const c10::cuda::CUDAGuard guard(q.device());
   check_status(indexer_scores(static_cast<const uint8_t*>(q.data_ptr()), weights.data_ptr<float>(), &cache,
