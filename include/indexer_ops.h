@@ -84,8 +84,10 @@ size_t indexer_cache_bytes(void);
  * s = scale * sin(angle), pair i = (a, b) becomes
  *   (a c - b s, b c + a s)   or, with transpose != 0, the gradient's (a c + b s, b c - a s),
  * computed in fp32 and rounded once. Columns outside [start, start + rot_dim) are copied.
- * Angles are exact to 2^-32 of a turn for any int32 position: freqs become 64-bit
- * fixed-point turns whose product with the position wraps.
+ * Angles keep their precision at any int32 position: freqs become 64-bit fixed-point turns
+ * whose product with the position wraps, which leaves them within 2^-31 of a turn (for
+ * frequencies of a few radians); sine and cosine are taken in fp32 of an angle that is
+ * rounded to 24 bits within an eighth of a turn, 2^-28 of a turn at most.
  * rot_dim even, 2 <= rot_dim, start >= 0, start + rot_dim <= dim <= 65536. */
 int indexer_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stride,
                    const int32_t* positions, const double* freqs, int32_t dtype, int64_t tokens,
@@ -130,7 +132,8 @@ int indexer_cache_read(const indexer_cache_t* cache, const int32_t* slots, int64
  * exact, sums are held in fp32. A NaN scale or weight makes its scores NaN (a block with
  * a value that is not finite has one); a NaN code on its own counts as a product of 0.
  * A page id outside [0, num_pages): its positions' scores are -inf, and each is counted
- * at least once.
+ * at least once. Scores around a wait that ran out are NaN (never, unless there is a bug;
+ * it is counted).
  * Needs 1 <= heads <= 128, row_len >= 1, and codes (pointer and strides) and q aligned to
  * 16 bytes. */
 int indexer_scores(const uint8_t* q, const float* weights, const indexer_cache_t* cache,

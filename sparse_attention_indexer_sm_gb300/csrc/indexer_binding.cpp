@@ -79,9 +79,9 @@ void check_vector(const Tensor& t, const char* name, ScalarType type, int64_t n,
     throw py::value_error(text(name, " must be a contiguous vector of length ", n));
 }
 
-// No operator has a forward-mode derivative: a tangent is refused, not dropped. Nor, `backward` says, has this one a
-// backward: an input that asks for a gradient is refused, not detached. Most tensors carry nothing that could say either,
-// and are done with after one look: the others' questions would cost each call 0.1 to 0.3 us.
+// No operator has a forward-mode derivative: a tangent is refused, not dropped. Nor, `backward` says, has this
+// one a backward: an input that asks for a gradient is refused, not detached. Most tensors carry nothing that
+// could say either, and are done with after one look: the others' questions would cost each call 0.1 to 0.3 us.
 void check_autograd(std::initializer_list<const Tensor*> tensors, bool backward) {
   for (const Tensor* t : tensors) {
     if (t == nullptr || t->unsafeGetTensorImpl()->autograd_meta() == nullptr) continue;
@@ -121,9 +121,9 @@ cudaStream_t stream_of(const Stream& stream, const Tensor& x) {
   return stream ? reinterpret_cast<cudaStream_t>(*stream) : c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
 }
 
-// An output. Of a call on a stream of the caller's it comes from that stream's memory: a block of the current stream's may
-// still be in use by work queued there, which `stream` is not behind. The current stream, where the caller goes on, counts
-// as a user of it: work queued there holds the block when the caller lets go of it.
+// An output. Of a call on a stream of the caller's it comes from that stream's memory: a block of the current
+// stream's may still be in use by work queued there, which `stream` is not behind. The current stream, where
+// the caller goes on, counts as a user of it: work queued there holds the block when the caller lets go of it.
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& x, const Stream& stream) {
   // straight from the caching allocator: at::empty's way through the dispatcher takes longer than the checks
   if (!stream) return at::detail::empty_cuda(shape, type, x.device(), std::nullopt);

@@ -8,12 +8,15 @@
 //   value lies on a border between codes up to the scale's own rounding, whose sign decides. A 32-bit
 //   value's remainder, which one fma gives exactly, becomes a sticky last bit: the quotient rounded to
 //   odd, which rounds to e4m3 as the real one does. With a power of two as the scale the quotient is exact.
-// - The split. Eight lanes own a block, 16 values each: with sixteen lanes of 8
-//   values what a lane does once a block (its place, its scale) cost as much as its values, and the kernel
-//   was bound by instructions (8192 x 64 rows of 128 in bf16: 60 us). The largest magnitude is
-//   found on the bit patterns, as integers, which order a NaN above everything. Reading back, a lane
-//   makes one 32-byte store of 16 or 8 columns (or 16-byte store of 8); eight CTAs an SM hide the loads' latency, which four rows in
-//   flight in each of fewer lanes did not (524288 rows of 512 to bf16: 132 against 203 us).
+// - The split. Eight lanes own a block, 16 values each: with sixteen lanes of 8 values what a lane does once a
+//   block (its place, its scale) cost as much as its values, and the kernel was bound by instructions
+//   (8192 x 64 rows of 128 in bf16: 60 us against 35). The largest magnitude is found on the bit patterns, as
+//   integers, which order a NaN above everything. In 32 bits the same rows take 51 us, 97% of the copy rate; a
+//   width that is no multiple of 8 is read and written value by value (rows of 63: 48 us, three times its
+//   floor).
+//   Reading back, a lane makes one 32-byte store of 16 or 8 columns (or 16-byte store of 8); eight CTAs an SM
+//   hide the loads' latency, which four rows in flight in each of fewer lanes did not (524288 rows of 512 to
+//   bf16: 131 against 203 us).
 
 #include <cuda_fp8.h>
 
@@ -290,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 8) read_kernel(const ReadParams p) {
   }
 }
 
-// Four times the CTAs that an SM holds, at most: enough rounds to even out uneven ones, few enough to keep a CTA's start
-// cheap (65535 rows of 576 written: 23.3 us with one time, 22.1 with four, 23.4 with eight; 524288 rows of 512 read: 140 us
-// with two, 132 with four).
+// Four times the CTAs that an SM holds, at most: enough rounds to even out uneven ones, few enough to keep a
+// CTA's start cheap (65535 rows of 576 written: 23.3 us with one time, 22.1 with four, 23.4 with eight; 524288
+// rows of 512 read: 140 us with two, 132 with four).
 unsigned grid_for(int64_t threads, int sms) {
   const int64_t blocks = (threads + kThreads - 1) / kThreads, most = int64_t(sms) * 32;
   return static_cast<unsigned>(blocks < most ? blocks : most);
@@ -462,8 +465,8 @@ int indexer_cache_read(const indexer_cache_t* cache, const int32_t* slots, int64
   p.scale_ps = cache->scale_page_stride;
   p.scale_ts = cache->scale_token_stride;
   p.capacity = static_cast<uint32_t>(cache->num_pages * cache->page_size);
-  // Columns of an item: a 32-byte store where rows start on 32 bytes, or eight, or one (239616 rows of 200 to bf16: eight
-  // 27 us, one 111).
+  // Columns of an item: a 32-byte store where rows start on 32 bytes, or eight, or one (239616 rows of 200 to
+  // bf16: eight 27 us, one 111).
   const int32_t wide = 32 / static_cast<int32_t>(dtype_bytes(dtype));
   auto fits = [&](int32_t n) {
     return p.dim % n == 0 && p.code_ts % n == 0 && p.code_ps % n == 0 && aligned(p.codes, n) &&

@@ -1,17 +1,21 @@
 // Rotary positions: pairs of columns turned by an angle of their own, position * frequency.
 //
 // Bound by memory: every element is read once and written once, with a few operations each.
-// - The angle. position * frequency in radians loses the fraction of a turn for far
-//   positions in fp32 (2^20 positions leave 4 bits of it), and GB300 has almost no fp64
-//   rate. A frequency's bits are therefore turned into a 64-bit fixed-point fraction of a turn by
-//   one integer product; position * fraction wraps modulo one turn by itself, without any
-//   rounding, and its top 32 bits are the angle.
-// - The split. A CTA owns a tile of tokens and heads. Its threads first leave the tile's sines and cosines
-//   in shared memory, each computed once, then walk over the rows in pieces of 32 bytes (interleaved) or twice 16 (half layout; twice 32 needs too
-//   many registers). Many small CTAs
-//   hide the loads' latency better than several pieces in flight in each thread (one piece and six CTAs an SM
-//   against two and five: 8192 x 64 x 128 in bf16, half of each row turned, 48 against 52 us). Sines kept in registers over a thread's heads took up to 232
-//   registers and left the loads' latency bare (8192 x 64 x 128 in bf16, half of each row turned: 89 us).
+// - The angle. position * frequency in radians loses the fraction of a turn for far positions in fp32 (2^20
+//   positions leave 4 bits of it), and GB300 has almost no fp64 rate. A frequency's bits are therefore turned
+//   into a 64-bit fixed-point fraction of a turn by one integer product, cut off at 2^-64; position * fraction
+//   wraps modulo one turn by itself, without any rounding, and its top 32 bits are the angle: within 2^-31 of a
+//   turn at any position, for frequencies of a few radians. Sine and cosine are taken of its 24 leading bits
+//   past a quarter's multiple, 2^-28 of a turn at most: the step of an fp32 angle within a turn.
+// - The split. A CTA owns a tile of tokens and heads. Its threads first leave the tile's sines and cosines in
+//   shared memory, each computed once, then walk over the rows in pieces of 32 bytes (interleaved) or twice 16
+//   (half layout; twice 32 needs too many registers). Many small CTAs hide the loads' latency better than
+//   several pieces in flight in each thread (one piece and six CTAs an SM against two and five: 8192 x 64 x 128
+//   in bf16, half of each row turned, 48 against 52 us). Sines kept in registers over a thread's heads took up to
+//   232 registers and left the loads' latency bare (the same rows: 89 us).
+// - A decode step (48 x 64 x 128: 3.0 us) is one chain: frequency and position behind the row's load, the
+//   64-bit product, the series, shared memory, a barrier, the store. Columns that pass through are a second loop
+//   behind that barrier (32768 rows of 192 in fp32, a third turned: 8.9 us where its bytes take 7.4).
 
 #include "indexer_common.cuh"
 
@@ -56,7 +60,8 @@ __device__ __forceinline__ uint64_t turn_step(double freq) {
 // series (the first terms left out are below 2e-9 and 2e-10), then turned by the quarters.
 __device__ __forceinline__ void sincos_turns(uint32_t u, float* sine, float* cosine) {
   const uint32_t quarters = (u + 0x20000000u) >> 30;
-  const float x = static_cast<float>(static_cast<int32_t>(u - (quarters << 30))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  constexpr float kRadians = 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float x = static_cast<float>(static_cast<int32_t>(u - (quarters << 30))) * kRadians;
   const float y = x * x;
   float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
   s = fmaf(s, y, 1.0f / 120.0f);
@@ -180,9 +185,9 @@ __global__ void __launch_bounds__(kThreads, resident(V * sizeof(T))) rotary_kern
 template <typename T>
 cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half, bool in_place, int sms,
                           cudaStream_t stream) {
-  // The widest accesses on whose boundaries every row starts, and the turned columns' parts: 32 bytes (interleaved
-  // only: 8191 x 64 x 128 in bf16 44 us against 52 with 16 bytes), 16, 4 (two 16-bit values: 4096 x 7 x 130, 68 columns
-  // turned, half layout, 7.7 us against 10.4 with single ones), or single values.
+  // The widest accesses on whose boundaries every row starts, and the turned columns' parts: 32 bytes
+  // (interleaved only: 8191 x 64 x 128 in bf16 44 us against 52 with 16 bytes), 16, 4 (two 16-bit values: 4096
+  // x 7 x 130, 68 columns turned, half layout, 7.7 us against 10.4 with single ones), or single values.
   const int64_t all = p.x_ts | p.x_hs | p.out_ts | p.out_hs | dim | p.start | (half ? p.all_pairs : 2 * p.all_pairs);
   const uintptr_t bases = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out);
   constexpr int kV = 16 / sizeof(T);
@@ -194,7 +199,8 @@ cudaError_t launch_rotary(RotaryParams p, int64_t tokens, int32_t dim, bool half
   const int64_t pairs = segments > 1 ? kMaxAngles : p.all_pairs;
   const int64_t turn_items = pairs / pairs_of_item, copy_items = in_place ? 0 : (dim - 2 * p.all_pairs) / v;
   // A CTA owns all heads of some tokens, or a part of one token's heads: from one piece to about eight for each
-  // thread, in whole rounds of the CTAs that the chip holds (a last round of a few CTAs takes as long as a full one).
+  // thread, in whole rounds of the CTAs that the chip holds (a last round of a few CTAs takes as long as a full
+  // one).
   const int64_t row = turn_items + copy_items, total = tokens * p.heads * row, slots = int64_t(sms) * resident(v * sizeof(T));
   const int64_t rounds = (total + slots * 8 * kThreads - 1) / (slots * 8 * kThreads);
   int64_t pieces = total / (slots * rounds);

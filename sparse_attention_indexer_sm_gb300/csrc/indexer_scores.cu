@@ -7,34 +7,36 @@
 // kind::f8f6f4. A key is a TMEM lane, so the thread that reads a lane holds all of its key's
 // products and sums its heads without any exchange between threads.
 //
-// What bounds it: one query a sequence (decode) reads 132 bytes a key for 2 * 128 * heads
-// operations and is bound by memory (256 rows of 32768 keys, 64 heads: 175 us, 6.5 TB/s); a prompt's chunk shares a
-// key tile between the queries of a group and is bound by the epilogue's relu-sum (2048 queries over 32768 keys: 512 us,
-// 2.14 PFLOP/s).
+// What bounds it: one query a sequence (decode) reads 132 bytes a key for 2 * 128 * heads operations and is
+// bound by memory (256 rows of 32768 keys, 64 heads: 175 us, 6.5 TB/s). A prompt's chunk shares a key tile
+// between the queries of a group and is bound by the epilogue's relu-sum (2048 queries over 32768 keys:
+// 512 us, 2.1 PFLOP/s); so are several drafted tokens (64 rows of 4 queries: 83 us against 46 for the memory).
 //
-// One CTA an SM, persistent: over items (sequence, query group, chunk of tiles) in turn, or over an equal span of all tiles
-// that some query sees, which each CTA finds by adding up the lengths. A tile's products are one unit of columns, or
-// two (the same number for a whole launch). The warps of a CTA share out the work:
+// One CTA an SM, persistent: over items (sequence, query group, chunk of tiles) in turn, or over an equal span
+// of all tiles that some query sees, which each CTA finds by adding up the lengths. A tile's products are one
+// unit of columns, or two (the same number for a whole launch). The warps of a CTA share out the work:
 //   loaders      page ids and TMA copies: a ring of key tiles, two buffers of queries
 //   multipliers  tcgen05.mma
 //   scalers      the keys' scales, two tiles at once: they are a dependent load behind the page id,
 //                which no warp with other work should wait for
 //   epilogue     groups of four warps, each with a weight for every one of its columns in registers: from
 //                shared memory a weight costs as much as four columns' arithmetic
-// in one of two plans. A lone warp takes some 50 cycles for each barrier that it looks at, so with up to 128 columns, where
-// a tile is soon done, every role that a tile passes through has two warps or four that take turns. With more
-// columns an epilogue group's work on a tile outlasts that, and what counts is how many warps hide each other's latencies: four
-// groups, of a quarter of the columns each (2048 queries over 32768 keys, 16 and 64 heads: 147 and 511 us against
-// 183 and 544 with two groups). There the epilogue still bounds the kernel, at 66% of the issue slots and 64% of the
-// integer pipe (relu is one of its instructions); the tensor pipe is at 43%. Its warps wait for a tile 5% of their time;
-// of some 200 instructions a warp and tile 96 are relus and products. Moving half of the relus to the fp32 pipe (a
-// saturating product) changed nothing, nor did larger or smaller loads from TMEM: what is left is latency.
-// A barrier's parity tells a phase from the next one, but not from the one after that. So each place of a
-// ring belongs to the same warp of a role throughout: tiles and units are dealt out by their running
-// numbers over the whole launch, and the rings' lengths are multiples of the numbers of warps.
-// A page is copied in pieces of the largest power of two of rows that divides its size, so every page size
-// takes the same path; but pages of one row are gathered, four by one copy (64 rows of 32768 keys, 64 heads:
-// 93 us against 238 with a copy for each).
+// in one of two plans. A lone warp takes some 50 cycles for each barrier that it looks at, so with up to 128
+// columns, where a tile is soon done, every role that a tile passes through has two warps or four that take
+// turns. With more columns an epilogue group's work on a tile outlasts that, and what counts is how many warps
+// hide each other's latencies: four groups, of a quarter of the columns each (2048 queries over 32768 keys, 16,
+// 32 and 64 heads: 151, 275 and 511 us, with two groups 183, 297 and 540). There the epilogue still bounds the
+// kernel, at 66% of the issue slots and 64% of the integer pipe (relu is one of its instructions); the tensor
+// pipe is at 43%. Its warps wait for a tile 5% of their time. Of some 200 instructions a warp and tile 96 are
+// relus and products and 54 are left in an epilogue without them; the rest, some 50, is not accounted for
+// (spilled registers, and places that are worked out at every tile, are among it). No pipe is full: the
+// instructions' own latencies are, and fewer of them would show.
+// A barrier's parity tells a phase from the next one, but not from the one after that. So each place of a ring
+// belongs to the same warp of a role throughout: tiles and units are dealt out by their running numbers over the
+// whole launch, and the rings' lengths are multiples of the numbers of warps.
+// A page is copied in pieces of the largest power of two of rows that divides its size, so every page size takes
+// the same path; but pages of one row are gathered, four by one copy (64 rows of 32768 keys, 64 heads: 90 us; a
+// copy for each took two and a half times that).
 
 #include <cuda.h>
 
@@ -49,9 +51,9 @@ namespace {
 constexpr int kDim = INDEXER_SCORE_DIM;  // bytes of a key's codes: one swizzled row
 constexpr int kTile = 128;               // keys of a tile: the rows of one MMA, the lanes of TMEM
 constexpr int kMaxColumns = 256;         // heads of a group's queries
-// How a CTA's warps share out its work, by the number of epilogue groups. Registers of a thread: what a launch of so many
-// threads has of 65536, moved from the first warps to the epilogue (512 * 128 = 256 * 64 + 256 * 192, and
-// 640 * 96 = 128 * 64 + 512 * 104).
+// How a CTA's warps share out its work, by the number of epilogue groups. Registers of a thread: what a launch
+// of so many threads has of 65536, moved from the first warps to the epilogue (512 * 128 = 256 * 64 + 256 * 192,
+// and 640 * 96 = 128 * 64 + 512 * 104).
 template <int kGroups> struct Plan;
 template <> struct Plan<2> {  // the groups take units in turn
   static constexpr int kLoaders = 2, kMultipliers = 2, kScalers = 4, kFewRegisters = 64, kManyRegisters = 192;
@@ -345,8 +347,8 @@ __device__ __forceinline__ int32_t seen_tiles(const ScoresParams& p, const Slice
   return tiles_of(clamped(p, longest));
 }
 
-// How a CTA walks over its work: items blockIdx.x, blockIdx.x + gridDim.x, ... of fixed chunks of tiles; or (kSpans) the
-// slices that its span of the tiles touches. Every role walks alike.
+// How a CTA walks over its work: items blockIdx.x, blockIdx.x + gridDim.x, ... of fixed chunks of tiles; or
+// (kSpans) the slices that its span of the tiles touches. Every role walks alike.
 template <bool kSpans> struct Walk;
 template <> struct Walk<false> {
   int64_t at;
@@ -367,8 +369,8 @@ template <> struct Walk<true> {
   }
 };
 
-// The place of the item at w, or the one after it. Items in turn are ordered with the chunk of tiles outermost, so that
-// the CTAs work on the same tiles of a sequence at about the same time and find them in L2.
+// The place of the item at w, or the one after it. Items in turn are ordered with the chunk of tiles outermost,
+// so that the CTAs work on the same tiles of a sequence at about the same time and find them in L2.
 template <bool kSpans>
 __device__ __forceinline__ Item place_at(const ScoresParams& p, const Walk<kSpans>& w, int ahead) {
   Item it = {};
@@ -415,8 +417,9 @@ __device__ __forceinline__ void item_ready(const ScoresParams& p, const Walk<kSp
   }
 }
 
-// This CTA's span: of all slices' tiles that are seen, in a row, with kItemCost more for each slice that has any, its
-// equal share. Every CTA adds up the same lengths by itself. All threads call this; `scratch` is of p.slices numbers.
+// This CTA's span: of all slices' tiles that are seen, in a row, with kItemCost more for each slice that has
+// any, its equal share. Every CTA adds up the same lengths by itself. All threads call this; `scratch` is of
+// p.slices numbers.
 __device__ __forceinline__ void find_span(const ScoresParams& p, Shared& s, int32_t* scratch) {
   const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int slices = static_cast<int>(p.slices), per = (slices + threads - 1) / threads;
@@ -443,8 +446,9 @@ __device__ __forceinline__ void find_span(const ScoresParams& p, Shared& s, int3
     before += k < warp ? v : 0;
     total += v;
   }
+  // where the span begins, and where the next one does; the last one ends with the last tile
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {  // where the span begins, and where the next one does; the last one ends with the last tile
+  for (int e = 0; e < 2; ++e) {
     const int32_t at = static_cast<int32_t>(static_cast<int64_t>(total) * (blockIdx.x + e) / gridDim.x);
     const int32_t look = at < total ? at : total - 1;
     if (look >= before && look < before + mine) {
@@ -460,8 +464,8 @@ __device__ __forceinline__ void find_span(const ScoresParams& p, Shared& s, int3
   __syncthreads();
 }
 
-// With spans: -inf into the tiles that no query of a slice sees. The chip's epilogue warps take blocks of 64 tiles in turn; a
-// lane looks a block up, the warp fills it.
+// With spans: -inf into the tiles that no query of a slice sees. The chip's epilogue warps take blocks of 64
+// tiles in turn; a lane looks a block up, the warp fills it.
 __device__ __forceinline__ void fill_rest(const ScoresParams& p, int64_t warp, int64_t warps) {
   constexpr int kBlock = 64;
   const int lane = threadIdx.x & 31;
@@ -573,15 +577,16 @@ __device__ __forceinline__ void load_keys(const ScoresParams& p, Shared& s, cons
     }
     tiles += it.seen - it.first;
   }
-  // no copy outlives the CTA (a place that was never used has not ended a phase, which its other parity says it has)
+  // no copy outlives the CTA (a place that was never used has not ended a phase, which its other parity says it
+  // has)
   for (uint32_t n = next_own; n < next_own + kKeyStages; n += kLoaders)
     bar_drain(&s.key_full[n % kKeyStages], (n / kKeyStages & 1u) ^ 1u);
   if (turn == 0)
     for (uint32_t n = items; n < items + 2; ++n) bar_drain(&s.query_full[n & 1], (n >> 1 & 1u) ^ 1u);
 }
 
-// The first tile of an item that is epilogue group `wg`'s, and the step to its next: with two groups every tile (two
-// units a tile) or every second one of the launch (one unit a tile), with four every tile.
+// The first tile of an item that is epilogue group `wg`'s, and the step to its next: with two groups every tile
+// (two units a tile) or every second one of the launch (one unit a tile), with four every tile.
 template <int kGroups>
 __device__ __forceinline__ int first_tile(const ScoresParams& p, const Item& it, int wg, uint32_t tiles) {
   return it.first + (kGroups == 2 && p.units == 1 ? static_cast<int>((wg ^ tiles) & 1u) : 0);
@@ -727,9 +732,9 @@ struct Lane {
   bool no_page;          // this key is on none
 };
 
-// Columns from C * kLoad on, which are on their way to r. With registers for it (two epilogue groups) the next load is
-// sent off before they are summed: 64 or 128 heads 4% faster; of four groups, whose warps hide it from one another, after.
-// Whether the next unit is there already: asked before the last sums, for use after them.
+// Columns from C * kLoad on, which are on their way to r. With registers for it (two epilogue groups) the next
+// load is sent off before they are summed: 64 or 128 heads 4% faster; of four groups, whose warps hide it from
+// one another, after. Whether the next unit is there already: asked before the last sums, for use after them.
 template <int kHeads, int kLoad, bool kWhole, int C, int kPairs>
 __device__ __forceinline__ bool columns_from(const ScoresParams& p, const Lane& l, const uint64_t (&w)[kPairs],
                                              float (&r)[kLoad], uint64_t acc0, uint64_t acc1) {
@@ -826,14 +831,15 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
     }
     const int count = min(max(it.count - first, 0), kQueries);
     l.columns = count * kHeads;
-    // every query of the group sees every key of the tiles that start here or before; of four groups, if all its columns
-    // are in use: no look at their number at each load (2048 queries of 16 heads 154 -> 148 us)
+    // every query of the group sees every key of the tiles that start here or before; of four groups, if all
+    // its columns are in use: no look at their number at each load (2048 queries of 16 heads 4% faster)
     const int whole = kGroups == 4 && count < kQueries ? -1 : it.shortest - kTile;
     l.lens = s.lens[warp] + first;
     const Item next_item = item_at(p, walk, 1);
     next_len = next_item.len;
     weights_of(next_item);  // on their way while this item is worked on
-    // The output's place goes on from tile to tile: worked out at each from a row's start, 2048 queries took 7% longer.
+    // The output's place goes on from tile to tile: worked out at each from a row's start, 2048 queries took 7%
+    // longer.
     const int step = tile_step<kGroups>(p), t0 = first_tile<kGroups>(p, it, wg, tiles);
     l.out = p.out + (it.query + first) * p.row_len + static_cast<int64_t>(t0) * kTile + tid;
     for (int t = t0; t < it.seen; t += step, l.out += step * kTile) {
@@ -876,8 +882,9 @@ __device__ __forceinline__ void reduce(const ScoresParams& p, Shared& s, uint32_
   }
 }
 
-// After a wait that ran out (rarely run, so out of line): NaN in place of every score that this epilogue warp has written. What is wrong among them was
-// read after the wait's end was noted.
+// After a wait that ran out: NaN in place of every score that this epilogue warp has written. What is wrong
+// among them was read after the wait's end was noted. Out of line, as no sound call comes here: inline, one
+// decode row's kernel took 3.95 us instead of 3.73.
 template <int kGroups, bool kSpans>
 __device__ __noinline__ void give_up(const ScoresParams& p, const Shared& s, int head_rows, int wg) {
   const int tid = threadIdx.x & 127, queries = Plan<kGroups>::kColumns / head_rows;
@@ -908,7 +915,7 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
 }
 
-// NaN in place of every score of a launch that cannot start (out of line too).
+// NaN in place of every score of a launch that cannot start; out of line too.
 __device__ __noinline__ void spoil(const ScoresParams& p) {
   begin_after_prior_grids();
   const int64_t all = p.slices / p.groups * p.queries * p.row_len, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -916,9 +923,10 @@ __device__ __noinline__ void spoil(const ScoresParams& p) {
     p.out[i] = __uint_as_float(kNan);
 }
 
-// Whether the dynamic shared memory starts where its declared alignment says, which the swizzled tiles rely on. Without a
-// rounding of its address every place in it is a constant, and the registers that held addresses are the epilogue's
-// (2048 queries over 32768 keys, 64 heads: 548 -> 512 us). If it ever starts elsewhere, all scores are NaN, and counted.
+// Whether the dynamic shared memory starts where its declared alignment says, which the swizzled tiles rely on.
+// Without a rounding of its address every place in it is a constant, and the registers that held addresses are
+// the epilogue's (2048 queries over 32768 keys, 64 heads: 548 -> 512 us). If it ever starts elsewhere, all
+// scores are NaN, and counted.
 __device__ __forceinline__ bool aligned_base(const ScoresParams& p, const Shared& s) {
   uint32_t base = smem_addr(&s);
   asm volatile("" : "+r"(base));
@@ -1120,9 +1128,9 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
   p.group = kMaxColumns / head_rows < queries ? kMaxColumns / head_rows : queries;
   p.groups = (queries + p.group - 1) / p.group;
   p.tiles = static_cast<int32_t>((row_len + kTile - 1) / kTile);
-  // Groups of queries of more than 128 columns, in columns of 16, 32 or 64 a query: four epilogue groups, a quarter of a
-  // tile's columns each, and one unit a tile; otherwise two, and units of up to 128 columns. (64 rows of 4 queries of 64
-  // heads, 32768 keys: 76 us with four, 79 with two.)
+  // Groups of queries of more than 128 columns, in columns of 16, 32 or 64 a query: four epilogue groups, a
+  // quarter of a tile's columns each, and one unit a tile; otherwise two, and units of up to 128 columns. (2048
+  // queries over 32768 keys, 64 heads: 511 us with four, 540 with two; 64 rows of 4 queries: 83.2 against 83.8.)
   const int columns = p.group * head_rows;
   const int epilogues = columns > 128 && head_rows <= 64 ? 4 : 2;
   p.unit_queries = epilogues == 4 ? p.group : Plan<2>::kColumns / head_rows;
@@ -1140,11 +1148,12 @@ extern "C" int indexer_scores(const uint8_t* q, const float* weights, const inde
     if (cost < best) best = cost, p.chunk = chunk;
   }
   p.items = p.slices * ((p.tiles + p.chunk - 1) / p.chunk);
-  // Equal spans of the tiles that are seen, whatever the lengths, instead of items in turn: adding the lengths up costs
-  // 1.7 us, so from 32 tiles an SM on, were all rows full, and from more with more slices than a CTA's threads read at
-  // once. Lengths even over the range: 64 rows of up to 32768 keys 30
-  // against 41 us, 256 rows 99 against 134, 8 of up to 262144 30 against 39 (48 of up to 8192, 20 tiles an SM: 11.2
-  // against 10.7); full rows, 4 of 262144 28.6 against 26.9, 256 of 32768 176 against 178.
+  // Equal spans of the tiles that are seen, whatever the lengths, instead of items in turn: adding the lengths
+  // up costs 1.7 us, so from 32 tiles an SM on, were all rows full, and from more with more slices than a CTA's
+  // threads read at once. Lengths even over the range: 64 rows of up to 32768 keys 31 against 39 us, 256 rows 103
+  // against 137, 8 of up to 262144 22 against 33 (48 of up to 8192, 20 tiles an SM, which take items in turn:
+  // 11.2 against 10.7). Prompts, whose later queries see more, gain too: 2048 queries 512 against 529. Full rows
+  // lose: 64 of 32768 keys 52.7 against 50.9, 4 of 262144 31.4 against 28.7; 256 of 32768 are even at 178.
   const bool spans = p.slices <= kMaxSpanSlices && p.slices * (p.tiles + kItemCost) <= INT32_MAX &&
                      p.slices * p.tiles >= int64_t(sms) * (32 + p.slices / 64);
 
