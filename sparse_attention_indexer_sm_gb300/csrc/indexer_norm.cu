@@ -4,6 +4,8 @@
 //
 // Bound by memory: a row is read once and stays in registers, so its mean, the differences from it (their squares are the
 // variance: no difference of large numbers), and the result cost no second read.
+// - The mean. The row's sum times 1 / dim is off by a few steps of fp32, which every difference would have; their sum, which
+//   comes with that of their squares, says by how much (stats_of; 1 us of 43 for 131071 rows of 128).
 // - The split. A row belongs to a group of 8 to 256 lanes, as few as hold it in at most 4 pieces of 16 bytes each:
 //   narrow rows need no barrier and no idle lanes, wide ones need few registers. Rows that fit no group (more than 8192
 //   columns of 16 bits) or start on no 16-byte boundary are read value by value, the longest of them several times.
@@ -39,6 +41,16 @@ struct NormParams {
   int32_t dim, params32;  // params32: fp32 parameters, else the rows' type
   float eps, inv_dim;
 };
+
+// A row's mean and 1 / sqrt(variance + eps). `about`: the sum of the row times 1 / dim, which is off by the sum's rounding and
+// by that of 1 / dim, a step or more of fp32 that each difference from it would have, times rstd (a constant row of 200 in 7168
+// columns came out as -0.015). sums: of the differences from `about`, and of their squares: the first one is what `about` lacks.
+__device__ __forceinline__ float2 stats_of(const NormParams& p, float about, const float (&sums)[2]) {
+  const float rest = sums[0] * p.inv_dim;
+  float var = sums[1] * p.inv_dim;
+  if (var < 3.0e38f) var = fmaxf(fmaf(-rest, rest, var), 0.0f);  // (an infinity or a NaN stays one)
+  return make_float2(about + rest, rsqrtf(var + p.eps));
+}
 
 __device__ __forceinline__ float param_at(const void* p, bool wide, int i, float) { return static_cast<const float*>(p)[i]; }
 template <typename T>
@@ -100,7 +112,7 @@ template <typename T, int V, int L, int P>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
   constexpr int kGroups = kThreads / L;
   constexpr bool kHold = P * V <= 16;  // the parameters stay in registers
-  __shared__ float scratch[2][1][kWarps];
+  __shared__ float scratch[2][1][kWarps], scratch2[2][2][kWarps];
   begin_after_prior_grids();
   const int lane = threadIdx.x % L;
   const bool wide = p.params32 != 0, shift = p.bias != nullptr;
@@ -135,23 +147,25 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
       }
     }
     group_sum<L, 1>(sum, scratch, turn);
-    const float mean = sum[0] * p.inv_dim;
-    float square[1] = {0.0f};
+    const float about = sum[0] * p.inv_dim;
+    float sums[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int q = 0; q < P; ++q) {
       const int col = (q * L + lane) * V;
       if (live && col < p.dim)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float d = to_float(raw[q].v[i]) - mean;
-          square[0] = fmaf(d, d, square[0]);
+          const float d = to_float(raw[q].v[i]) - about;
+          sums[0] += d;
+          sums[1] = fmaf(d, d, sums[1]);
         }
     }
-    group_sum<L, 1>(square, scratch, turn);
-    const float rstd = rsqrtf(fmaf(square[0], p.inv_dim, p.eps));
+    group_sum<L, 2>(sums, scratch2, turn);
+    const float2 stat = stats_of(p, about, sums);
+    const float mean = stat.x, rstd = stat.y;
     if (!live) continue;
     if (p.stats != nullptr && lane == 0)
-      *reinterpret_cast<float2*>(p.stats + 2 * static_cast<int64_t>(row)) = make_float2(mean, rstd);
+      *reinterpret_cast<float2*>(p.stats + 2 * static_cast<int64_t>(row)) = stat;
     T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.dim;
 #pragma unroll
     for (int q = 0; q < P; ++q) {
@@ -170,24 +184,26 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
 // Any row, one a CTA, read three times (from L1 or L2 after the first).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_long_kernel(const NormParams p) {
-  __shared__ float scratch[2][1][kWarps];
+  __shared__ float scratch[2][1][kWarps], scratch2[2][2][kWarps];
   begin_after_prior_grids();
   const bool wide = p.params32 != 0;
   int turn = 0;
   for (uint32_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* src = row_at<T>(p.x, p, row, p.x_ts, p.x_hs);
-    float sum[1] = {0.0f}, square[1] = {0.0f};
+    float sum[1] = {0.0f}, sums[2] = {0.0f, 0.0f};
     for (int c = threadIdx.x; c < p.dim; c += kThreads) sum[0] += to_float(src[c]);
     group_sum<kThreads, 1>(sum, scratch, turn);
-    const float mean = sum[0] * p.inv_dim;
+    const float about = sum[0] * p.inv_dim;
     for (int c = threadIdx.x; c < p.dim; c += kThreads) {
-      const float d = to_float(src[c]) - mean;
-      square[0] = fmaf(d, d, square[0]);
+      const float d = to_float(src[c]) - about;
+      sums[0] += d;
+      sums[1] = fmaf(d, d, sums[1]);
     }
-    group_sum<kThreads, 1>(square, scratch, turn);
-    const float rstd = rsqrtf(fmaf(square[0], p.inv_dim, p.eps));
+    group_sum<kThreads, 2>(sums, scratch2, turn);
+    const float2 stat = stats_of(p, about, sums);
+    const float mean = stat.x, rstd = stat.y;
     if (p.stats != nullptr && threadIdx.x == 0)
-      *reinterpret_cast<float2*>(p.stats + 2 * static_cast<int64_t>(row)) = make_float2(mean, rstd);
+      *reinterpret_cast<float2*>(p.stats + 2 * static_cast<int64_t>(row)) = stat;
     T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.dim;
     for (int c = threadIdx.x; c < p.dim; c += kThreads)
       dst[c] = from_float<T>(fmaf((to_float(src[c]) - mean) * rstd, param_at(p.weight, wide, c, T()),

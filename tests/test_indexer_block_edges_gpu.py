@@ -1,0 +1,102 @@
+"""Edges of the layer norm, the appends to a block-scaled cache and the attention over it (needs a
+GB300): means of widths whose reciprocal fp32 does not have, codes at borders between two of them,
+NaN codes wherever the work is cut, caches without pages, captured gradients."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+E4M3 = torch.float8_e4m3fn
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+@pytest.fixture(scope="module")
+def fw():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_attention_indexer_sm_gb300 as p
+    p.load_library()
+    return p
+
+
+@pytest.fixture(autouse=True)
+def no_guard_hits(fw):
+    fw.indexer_reset_guard_hits()
+    yield
+    assert fw.indexer_guard_hits() == 0
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ---------------------------------------------------------------- layer norm
+
+# widths of every split of the rows over lanes, most of them without an exact reciprocal: by pieces of 16 bytes, value by
+# value, and long rows of both kinds
+DIMS = [24, 112, 200, 1000, 1536, 3584, 7168, 8200, 20000, 3, 31, 127, 1001, 5001]
+ROWS = [200.0, 1000.0, -7.0, 0.0703125, 3.0, 1.0 / 3.0, -60000.0]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_norm_of_constant_rows(fw, dim, dtype):
+    """A constant row is its shift, and gives the weight no gradient, to the last bit. (The mean that the row's sum gives is
+    off by a few steps of fp32; the differences from it are exact, all alike and a whole number of steps, so what it lacks is
+    known to within 2^-22 of those few steps, and the corrected mean is the row's value.)"""
+    x = torch.tensor(ROWS).to(dtype)[:, None].expand(-1, dim).contiguous().cuda().requires_grad_(True)
+    g = gen(dim)
+    w = torch.randn(dim, generator=g).cuda().requires_grad_(True)
+    b = torch.randn(dim, generator=g).to(dtype).float().cuda()
+    dy = torch.randn((len(ROWS), dim), generator=g).to(dtype).cuda()
+    y = fw.indexer_layer_norm(x, w, b, eps=1e-6)
+    assert torch.equal(y, b.to(dtype).expand_as(y))
+    assert not fw.indexer_layer_norm(x.detach(), w.detach(), eps=1e-6).any()
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    assert not dw.any()
+    # dx = (gw - mean(gw)) / sqrt(eps): products, their sum of up to 40 + dim / 256 additions in a row, the mean, the root
+    gw = dy.double().cpu() * w.detach().double().cpu()
+    rstd = 1e-6 ** -0.5
+    want = (gw - gw.mean(-1, keepdim=True)) * rstd
+    tol = rstd * U * (6 * gw.abs() + (50 + dim / 256) * gw.abs().mean(-1, keepdim=True))
+    half, tiny = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    fits = want.abs() < 0.9 * torch.finfo(dtype).max
+    assert ((dx.double().cpu() - want).abs() <= tol + (want.abs() + tol) * half + tiny)[fits].all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_norm_of_nearly_constant_rows(fw, dim, dtype):
+    """All values but a few are one large number. The mean is rounded once to fp32, whatever the width: it is off by half a step,
+    and by DEPTH additions of differences that are small."""
+    depth = 50 + dim / 256
+    x = torch.tensor(ROWS).to(dtype)[:, None].repeat(1, dim)
+    g = gen(dim + 1)
+    at = torch.randint(0, dim, (len(ROWS), max(1, dim // 50)), generator=g)
+    x.scatter_(1, at, (x.gather(1, at).float() * (1 + 4 * torch.finfo(dtype).eps)).to(dtype))
+    w = torch.randn(dim, generator=g)
+    eps = 1e-6
+    y = fw.indexer_layer_norm(x.cuda(), w.cuda(), eps=eps).double().cpu()
+    x, w = x.double(), w.double()
+    mean = x.mean(-1, keepdim=True)
+    d = x - mean
+    var = d.square().mean(-1, keepdim=True)
+    rstd = (var + eps).rsqrt()
+    first = (depth + 2) * U * x.abs().mean(-1, keepdim=True)  # how far the first mean may be off
+    spread = d.abs().mean(-1, keepdim=True) + first
+    e_mean = U * mean.abs() + (depth + 4) * U * spread
+    # squares around the first mean, less the square of what it lacked
+    e_var = (depth + 8) * U * (var + first.square()) + 4 * U * first * spread * (depth + 4)
+    r_rstd = 0.5 * e_var / (var + eps) + 4 * U
+    n = d * rstd
+    tol = (rstd * (e_mean + U * d.abs()) + n.abs() * (r_rstd + r_rstd.square() + 3 * U)) * w.abs()
+    want = n * w
+    half, tiny = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    worst = ((y - want).abs() / (tol + (want.abs() + tol) * half + tiny)).max().item()
+    assert worst <= 1.0, f"off by {worst:.3g} of the tolerance"
