@@ -3,15 +3,17 @@
 // A block's scale is the smallest power of two that brings its largest value to 448 or less. Tokens come a few at a time,
 // so a block that has rows from before keeps its scale unless the new rows need a larger one; then the older codes
 // are rounded once more, to old / new of what they were. That quotient is a power of two: codes that stay normal numbers
-// lose nothing that the new rows' precision has, whereas a scale of 24 bits would move every one of them.
+// lose nothing that the new rows' precision has, whereas a scale of 24 bits would move every one of them. A scale that something
+// else has written may be any number: products and quotients are then rounded to odd before they become codes, which
+// rounds them as the real ones.
 //
 // Bound by memory: rows are read once and codes written once. A warp, or the eight of a CTA, owns the part of one block
 // and head that a call appends, holds its rows in registers (the first eight of a lane, or four; more than those are read
 // again), agrees on the largest magnitude and writes. So nothing is exchanged between owners, and no order matters.
 // An owner's rows are behind the lengths of its sequence, which it finds among all by steps of 32 at once; and its page and
 // old scale are asked for with the rows.
-// Measured: 41000 rows of 8 heads of 128 in bf16 onto eight sequences 25 us (127 MB: 19 us at the copy rate), a token on each
-// of 256 sequences 4.4 us, a chain of four dependent loads (starts, lengths, page, scale and codes) around a launch.
+// Measured: 41000 rows of 8 heads of 128 in bf16 onto eight sequences 26 us (127 MB: 19 us at the copy rate), a token on each
+// of 256 sequences 4.5 us, a chain of four dependent loads (starts, lengths, page, scale and codes) around a launch.
 
 #include <cuda_fp8.h>
 
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : kJoin > 1 ? 5 :
   if ((old_bits & 0x7fffffffu) > kInfBits) bits = kNanBits;
   else if (bits != kNanBits && old > __uint_as_float(bits)) bits = old_bits;
   const float scale = __uint_as_float(bits), inv = 1.0f / scale;
+  const bool power = (bits & 0x7fffffu) == 0u || top >= kInfBits;  // x * inv is the quotient; or all is NaN
   if (at.before > 0 && bits != old_bits) {
     const float ratio = old / scale;
     for (uint32_t r = first; in && r < at.before; r += step) {
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : kJoin > 1 ? 5 :
         for (int k = 0; k < 2; ++k) {
           const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * k)), __NV_E4M3);
           const float2 f = __half22float2(__half2(h));
-          y |= e4m3x2(f.x * ratio, f.y * ratio) << (16 * k);
+          y |= e4m3x2(product_to_odd(f.x, ratio), product_to_odd(f.y, ratio)) << (16 * k);
         }
         now[i] = y;
       }
@@ -227,10 +230,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : kJoin > 1 ? 5 :
     T typed[kPiece];
     memcpy(typed, raw, sizeof(typed));
     uint32_t c[2];
+    if (power) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      c[i] = e4m3x2(to_float(typed[4 * i]) * inv, to_float(typed[4 * i + 1]) * inv) |
-             e4m3x2(to_float(typed[4 * i + 2]) * inv, to_float(typed[4 * i + 3]) * inv) << 16;
+      for (int i = 0; i < 2; ++i)
+        c[i] = e4m3x2(to_float(typed[4 * i]) * inv, to_float(typed[4 * i + 1]) * inv) |
+               e4m3x2(to_float(typed[4 * i + 2]) * inv, to_float(typed[4 * i + 3]) * inv) << 16;
+    } else {
+      auto code = [&](int k) { return quotient_to_odd(to_float(typed[k]), scale, inv); };
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = e4m3x2(code(4 * i), code(4 * i + 1)) | e4m3x2(code(4 * i + 2), code(4 * i + 3)) << 16;
+    }
     *reinterpret_cast<uint2*>(code + r * p.code_ts) = make_uint2(c[0], c[1]);
   };
 #pragma unroll

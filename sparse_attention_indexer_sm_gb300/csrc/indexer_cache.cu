@@ -59,20 +59,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// x / scale rounded to odd: exact, or with its last bit set and between the same two
-// 24-bit neighbours as the real quotient. `inv` is 1 / scale.
-__device__ __forceinline__ float quotient_to_odd(float x, float scale, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, scale, x), inv, q);
-  const float rest = fmaf(-q, scale, x);
-  uint32_t bits = __float_as_uint(q);
-  if (rest != 0.0f) {
-    bits -= (bits ^ __float_as_uint(rest)) >> 31;  // the rest points to zero: the lower neighbour
-    bits |= 1u;
-  }
-  return __uint_as_float(bits);
-}
-
 // top / 448, correctly rounded (Markstein: a quotient from the correctly rounded reciprocal, corrected once by its
 // exact remainder).
 __device__ __forceinline__ float over_448(float top) {

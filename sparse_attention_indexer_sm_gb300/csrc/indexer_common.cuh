@@ -63,6 +63,30 @@ inline bool block_cache_ok(const indexer_block_cache_t* c) {
          (reinterpret_cast<uintptr_t>(c->scales) & 3u) == 0;
 }
 
+// A result q that lacks `rest`, rounded to odd: exact, or with its last bit set and between the same two 24-bit neighbours as
+// the real result. It rounds to fewer bits as that one does.
+__device__ __forceinline__ float to_odd(float q, float rest) {
+  uint32_t bits = __float_as_uint(q);
+  if (rest != 0.0f) {
+    bits -= (bits ^ __float_as_uint(rest)) >> 31;  // the rest points to zero: the lower neighbour
+    bits |= 1u;
+  }
+  return __uint_as_float(bits);
+}
+
+// x / scale rounded to odd. `inv` is 1 / scale.
+__device__ __forceinline__ float quotient_to_odd(float x, float scale, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, scale, x), inv, q);
+  return to_odd(q, fmaf(-q, scale, x));
+}
+
+// a * b rounded to odd.
+__device__ __forceinline__ float product_to_odd(float a, float b) {
+  const float q = a * b;
+  return to_odd(q, fmaf(a, b, -q));
+}
+
 // Division of numbers below 2^31 by a constant of the launch: n / d = (n * magic) >> (31 + shift).
 struct Divisor {
   uint32_t d, magic, shift;

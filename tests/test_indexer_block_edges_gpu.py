@@ -9,6 +9,8 @@ import math
 import pytest
 
 torch = pytest.importorskip("torch")
+from test_indexer_attention_gpu import append_ref, make_cache, same  # noqa: E402
+
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
@@ -100,3 +102,66 @@ def test_norm_of_nearly_constant_rows(fw, dim, dtype):
     half, tiny = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
     worst = ((y - want).abs() / (tol + (want.abs() + tol) * half + tiny)).max().item()
     assert worst <= 1.0, f"off by {worst:.3g} of the tolerance"
+
+
+# ---------------------------------------------------------------- appends
+
+def borders():
+    """Halfway between neighbouring e4m3 values, normal ones."""
+    grid = torch.arange(8, 127, dtype=torch.uint8).view(E4M3).float().double()
+    return (grid[1:] + grid[:-1]) / 2
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [4, 64])
+def test_append_under_scales_that_are_no_powers_of_two(fw, block, dtype):
+    """Blocks whose scale from before is any number: quotients within a step of fp32 of a border between two codes, above it,
+    below it and on it, become the code that is nearest to the real quotient."""
+    pages, heads, dim, rows = 300, 2, 128, 3
+    g = gen(block)
+    codes, scales = make_cache(g, pages, block, heads, dim, block)
+    mids = borders()
+    shape = (pages, heads)
+    at = torch.rand(shape, generator=g).add(1.0).to(dtype).double() * 2.0 ** -3  # a value of the row's type, and its border
+    m = mids[torch.randint(24, 109, shape, generator=g)]  # below 224: half of what the scale holds, so none grows
+    s = (at / m).float()
+    # that value times powers of two, and for fp32 its neighbours too; all of them within what the scale holds
+    x = at[:, None, :, None] * torch.exp2(torch.randint(-5, 1, (pages, rows, heads, dim), generator=g).double())
+    x = x * (torch.randint(0, 2, x.shape, generator=g).double() * 2 - 1)
+    x = x.float()
+    if dtype == torch.float32:
+        x = torch.nextafter(x, torch.full_like(x, 1e9) * torch.randint(-1, 2, x.shape, generator=g).float() + x)
+    x = x.to(dtype).flatten(0, 1).cuda()
+    starts = (torch.arange(pages + 1) * rows).int().cuda()
+    lens = torch.full((pages,), rows + 1, dtype=torch.int32).cuda()  # one position is there already
+    table = torch.randperm(pages, generator=g).int().view(pages, 1)
+    scales[table[:, 0].long(), 0] = s.cuda()
+    args = (x, starts, lens, table.cuda(), codes, scales)
+    ref = append_ref(*args)
+    assert torch.equal(ref[1][:, 0][table[:, 0].long()], s.double())  # the scales stay
+    fw.indexer_cache_append(*args)
+    same(codes, scales, ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_append_where_any_scale_grows(fw, dtype):
+    """Codes from before that come near a border between two codes as their scale, any number, gives way to a power of two."""
+    pages, heads, dim, block = 300, 2, 128, 8
+    g = gen(5)
+    codes, scales = make_cache(g, pages, block, heads, dim, block)
+    grid = torch.arange(8, 127, dtype=torch.uint8).view(E4M3).float().double()
+    mids = borders()
+    c = grid[torch.randint(0, len(grid), (pages, heads), generator=g)]
+    s = (mids[torch.randint(0, len(mids), (pages, heads), generator=g)] / c).float()
+    s = s * torch.exp2(-6 - torch.frexp(s)[1].float())  # 2^-7 to 2^-6: the power of two takes its place
+    scales[:, 0] = s.cuda()
+    codes[:, :3] = (c[:, None, :, None] * (torch.randint(0, 2, (pages, 3, heads, dim), generator=g).double() * 2 - 1)).float().to(E4M3).cuda()
+    x = torch.full((pages, heads, dim), 5.0).to(dtype).cuda()
+    starts = torch.arange(pages + 1).int().cuda()
+    lens = torch.full((pages,), 4, dtype=torch.int32).cuda()
+    table = torch.arange(pages, dtype=torch.int32).view(pages, 1).cuda()
+    args = (x, starts, lens, table, codes, scales)
+    ref = append_ref(*args)
+    assert (ref[1] == 2.0 ** -6).all()
+    fw.indexer_cache_append(*args)
+    same(codes, scales, ref)
