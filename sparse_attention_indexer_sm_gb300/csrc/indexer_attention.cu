@@ -779,7 +779,7 @@ int indexer_attention(const void* q, int32_t dtype, const indexer_block_cache_t*
   constexpr int64_t kLongest = INT32_MAX - 65536;  // steps are numbered in 31 bits
   p.fp16 = dtype == INDEXER_FP16;
   p.whole_steps = seq_lens != nullptr && keys->page_size % kStep == 0;
-  p.row_len = static_cast<int32_t>(keys->num_pages == 0 ? 0 : seq_lens == nullptr ? width : width > kLongest / keys->page_size ? kLongest : width * keys->page_size);
+  p.row_len = static_cast<int32_t>(seq_lens == nullptr ? width : width > kLongest / keys->page_size ? kLongest : width * keys->page_size);
   p.scale = softmax_scale * 1.44269504088896340736f;
   return status_of(run_attention(p, sms, stream));
 }

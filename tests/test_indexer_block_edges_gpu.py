@@ -165,3 +165,28 @@ def test_append_where_any_scale_grows(fw, dtype):
     assert (ref[1] == 2.0 ** -6).all()
     fw.indexer_cache_append(*args)
     same(codes, scales, ref)
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("size", [16, 5])
+@pytest.mark.parametrize("group,dim", [(3, 64), (20, 128), (40, 128), (100, 128), (200, 112), (4, 256)])
+def test_attention_over_a_cache_without_pages(fw, group, dim, size):
+    """Every slot and page id is outside it: nothing is seen, and each that is asked for is counted."""
+    codes, scales = torch.empty((0, size, 2, dim), dtype=torch.uint8, device="cuda").view(E4M3), torch.empty((0, 1, 2), device="cuda")
+    cache = (codes, scales, codes.clone(), scales.clone())
+    q = torch.randn((3, 2, 2 * group, dim), generator=gen(1)).bfloat16().cuda()
+    slots = torch.full((6, 300), -1, dtype=torch.int32)
+    slots[0, 7], slots[1, ::2], slots[3, 299], slots[5, 0] = 0, 3, 2**31 - 1, -2
+    out, lse = fw.indexer_attention(q, *cache, slots=slots.cuda(), return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert fw.indexer_guard_hits() >= 153
+    fw.indexer_reset_guard_hits()
+    assert not fw.indexer_attention(q, *cache, slots=torch.full_like(slots, -1).cuda()).any()
+    assert fw.indexer_guard_hits() == 0  # none is asked for
+    table = torch.tensor([[0, 1, 2, 3], [-1, 7, 0, 0], [0, 0, 0, 0]], dtype=torch.int32).cuda()
+    lens = torch.tensor([[3 * size, 4 * size], [1, 2], [0, 0]], dtype=torch.int32).cuda()
+    out, lse = fw.indexer_attention(q, *cache, page_table=table, seq_lens=lens, return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert fw.indexer_guard_hits() >= 5
+    fw.indexer_reset_guard_hits()
