@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <algorithm>
@@ -18,7 +19,9 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <unordered_set>
 #include <utility>
+#include <vector>
 
 #include "indexer_ops.h"
 
@@ -142,21 +145,54 @@ void written(const Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-// A differentiable call under capture whose leaf has a gradient graph from before, made on the default stream, is
-// refused: that graph's node for the leaf would take the captured backward to the default stream, which no capture
-// can hold, and torch ends the process over it.
+// A node of a gradient graph from before that was made on the default stream would take a captured backward there, which no
+// capture can hold, and torch ends the process over it. So a differentiable call under capture is refused if one of its
+// leaves has such a node already; and a captured backward, whatever the call's inputs were made from, if one of the nodes
+// that it goes on to is one.
+constexpr const char* kHeldGraph = "capture: a tensor of the call still belongs to a gradient graph of the default stream (let go of its results first)";
+
+bool on_default_stream(torch::autograd::Node& node) {
+  const auto stream = node.stream();
+  return stream && stream->id() == c10::cuda::getDefaultCUDAStream(stream->device_index()).unwrap().id();
+}
+
+bool capturing(const Tensor& t) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(stream_of(Stream(), t), &status) == cudaSuccess && status != cudaStreamCaptureStatusNone;
+}
+
 void check_capture(std::initializer_list<const Tensor*> tensors) {
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  bool known = false;
   for (const Tensor* t : tensors) {
     if (t == nullptr || !t->requires_grad() || !t->is_leaf()) continue;
-    if (capturing == cudaStreamCaptureStatusNone &&
-        (cudaStreamIsCapturing(stream_of(Stream(), *t), &capturing) != cudaSuccess || capturing == cudaStreamCaptureStatusNone))
-      return;
+    if (!known && !capturing(*t)) return;
+    known = true;
     const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-    if (node == nullptr) continue;
-    const auto stream = node->stream();
-    if (stream && stream->id() == c10::cuda::getDefaultCUDAStream(t->device().index()).unwrap().id())
-      throw py::value_error("capture: a tensor of the call still belongs to a gradient graph of the default stream (let go of its results first)");
+    if (node != nullptr && on_default_stream(*node)) throw py::value_error(kHeldGraph);
+  }
+}
+
+// In a backward, before it launches anything.
+void check_captured_backward(const Tensor& grad) {
+  if (!capturing(grad)) return;
+  const auto here = torch::autograd::get_current_node();
+  const auto* wanted = torch::autograd::get_current_graph_task_exec_info();  // empty: all nodes run
+  if (here == nullptr) return;
+  std::vector<torch::autograd::Node*> open = {here.get()};
+  std::unordered_set<torch::autograd::Node*> seen = {here.get()};
+  while (!open.empty()) {
+    torch::autograd::Node* const node = open.back();
+    open.pop_back();
+    for (const auto& edge : node->next_edges()) {
+      torch::autograd::Node* const next = edge.function.get();
+      if (next == nullptr || !seen.insert(next).second) continue;
+      if (wanted != nullptr && !wanted->empty()) {
+        const auto found = wanted->find(next);
+        if (found == wanted->end() || !found->second.should_execute()) continue;
+      }
+      if (on_default_stream(*next)) throw py::value_error(kHeldGraph);
+      open.push_back(next);
+    }
   }
 }
 
@@ -205,6 +241,7 @@ struct Rotary : torch::autograd::Function<Rotary> {
                                                  torch::autograd::variable_list grads) {
     Tensor grad = grads[0];
     if (grad.defined()) {
+      check_captured_backward(grad);
       if (grad.size(-1) > 1 && grad.stride(-1) != 1) grad = grad.contiguous();
       const auto saved = ctx->get_saved_variables();
       const std::optional<Tensor> axes = saved[2].defined() ? std::optional<Tensor>(saved[2]) : std::nullopt;
@@ -295,6 +332,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
                                                  torch::autograd::variable_list grads) {
     if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor()};
     require(!at::GradMode::is_enabled(), "indexer_layer_norm has no second derivative: call backward without create_graph");
+    check_captured_backward(grads[0]);
     const auto saved = ctx->get_saved_variables();
     const Tensor &x = saved[0], &weight = saved[1], &stats = saved[2];
     Tensor grad = grads[0];

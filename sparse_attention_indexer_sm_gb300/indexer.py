@@ -231,7 +231,11 @@ def indexer_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor
     transpose: the rotation of a gradient (by the opposite
     angle, with the same scale). out: a tensor like x, or x itself for a call in place.
     Differentiable in x by backward (twice too); a call with `out` or `stream` is not, and
-    forward-mode tangents are refused."""
+    forward-mode tangents are refused. Under capture a differentiable call refuses an x that is a
+    leaf of a gradient graph of the default stream that is still held (by its results, or by a
+    hook), and its backward refuses to go on to any node of such a graph, whatever x was made
+    from: torch would end the process. Let go of that graph first, or call under
+    torch.no_grad() where no gradient is wanted."""
     f = (_binding or _load_binding()).rotary
     how = _choice(layout, _LAYOUTS, "layout")
     if stream is not None:
@@ -251,8 +255,9 @@ def indexer_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     rounded once. out: a contiguous tensor like x that does not overlap it. Differentiable in
     x, weight and bias by backward, once (the sums of the parameters' gradients run in an order
     that the sizes decide: the same gradients in every run); a call with `out` or `stream` is
-    not, and forward-mode tangents are refused. Under capture a leaf must not belong to a
-    gradient graph of the default stream that is still held (as in indexer_rotary)."""
+    not, and forward-mode tangents are refused. Under capture neither the leaves nor what the
+    inputs were made from may belong to a gradient graph of the default stream that is still held:
+    the call or its backward is refused (as in indexer_rotary)."""
     f = (_binding or _load_binding()).layer_norm
     if stream is not None:
         return _on(stream, f, x, weight, bias, eps, out)

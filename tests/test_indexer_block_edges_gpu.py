@@ -190,3 +190,53 @@ def test_attention_over_a_cache_without_pages(fw, group, dim, size):
     assert not out.any() and (lse == -math.inf).all()
     assert fw.indexer_guard_hits() >= 5
     fw.indexer_reset_guard_hits()
+
+
+# ---------------------------------------------------------------- captured gradients
+
+@pytest.mark.parametrize("made", ["in the capture", "before it"])
+@pytest.mark.parametrize("name", ["norm", "rotary"])
+def test_captured_backward_to_a_graph_of_the_default_stream(fw, name, made):
+    """Inputs made from a leaf that such a graph holds: the backward is refused, before torch meets the default stream; the
+    forward alone can be captured, and all of it once that graph is gone."""
+    leaf = torch.randn((30, 64), generator=gen(3)).cuda().requires_grad_(True)
+    w, dy = torch.randn(64, generator=gen(4)).cuda(), torch.randn((30, 64), generator=gen(5)).cuda()
+    freqs, _ = fw.indexer_rotary_freqs(64)
+    positions = torch.arange(30, dtype=torch.int32).cuda()
+    call = {"norm": lambda x: fw.indexer_layer_norm(x, w), "rotary": lambda x: fw.indexer_rotary(x, positions, freqs)}[name]
+    held = leaf * 3.0
+    want = call(leaf.detach() * 3.0)
+    for wanted in ("leaf", "all"):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            x = held if made == "before it" else leaf * 3.0
+            y = call(x)
+            with pytest.raises(RuntimeError, match="gradient graph"):
+                if wanted == "leaf":
+                    torch.autograd.grad(y, leaf, dy)
+                else:
+                    y.backward(dy)
+            y = y.detach()
+        graph.replay()
+        assert torch.equal(y, want) and leaf.grad is None
+        del x
+    want = torch.autograd.grad(call(held), leaf, dy)[0]  # nothing is captured: as ever
+    del held
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(call(leaf * 3.0), leaf, dy)[0]
+    graph.replay()
+    assert torch.equal(got, want)
+
+
+def test_captured_backward_past_a_graph_of_the_default_stream(fw):
+    """Only the nodes that the backward goes on to matter: a weight's gradient alone, though the rows come from a held graph."""
+    leaf = torch.randn((30, 64), generator=gen(6)).cuda().requires_grad_(True)
+    w = torch.randn(64, generator=gen(7)).cuda().requires_grad_(True)
+    dy = torch.randn((30, 64), generator=gen(8)).cuda()
+    held = leaf * 3.0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(fw.indexer_layer_norm(held, w), w, dy)[0]
+    graph.replay()
+    assert torch.equal(got, torch.autograd.grad(fw.indexer_layer_norm(held, w), w, dy)[0])
