@@ -253,7 +253,9 @@ int indexer_cache_append(const void* x, int64_t x_token_stride, int64_t x_head_s
  * split of the work depends on the sizes, the lengths and the device: the same call gives the
  * same bits, another batch around a query may change its last ones.
  * Scales of values are taken as at least 2^-100 (a negative one too), and keys that no query
- * sees may hold anything.
+ * sees may hold anything. For the queries that see the key, a NaN code of a value makes its
+ * column NaN, however little the key weighs, and nothing else; a NaN among a key's codes or the
+ * key's or value's scales makes the row NaN, and its lse.
  * workspace: indexer_attention_workspace_bytes of the current device, 16-byte aligned; the call
  * enqueues two kernels. */
 int indexer_attention(const void* q, int32_t dtype, const indexer_block_cache_t* keys,

@@ -113,6 +113,34 @@ __device__ __forceinline__ void weigh(float (&o)[kDim / 16][kTiles][4], const ui
   }
 }
 
+// What weigh left out of `bad` keys (of a step from position j0 on): a NaN code of a value makes its column NaN for the rows that see
+// the key, and nothing else. columns: for each of the warp's rows, row0 on, a bit for each column, in shared memory, which the tile's
+// end looks at. A call, as its registers would be spilled in the loop (64 sequences of up to 8192 keys of 8 heads of 256 columns, 16
+// query heads on each: 307 us, 294 so).
+template <int kDim, int kWarpRows>
+__device__ __noinline__ void mark(const AttendParams& p, uint32_t* columns, uint32_t bad, const uint8_t* values, int32_t j0, int32_t list,
+                                  int32_t row0) {
+  using S = Shape<kDim>;
+  const int lane = threadIdx.x & 31, chunk = lane % S::kChunks;  // a lane a piece of the key's row
+  int32_t len = INT32_MAX;
+  if (p.seq_lens != nullptr && lane < kWarpRows && row0 + lane < p.list_queries * static_cast<int32_t>(p.group.d))
+    len = p.seq_lens[static_cast<int64_t>(list) * p.list_queries + quotient(p.group, row0 + lane)];
+#pragma unroll 1
+  for (; bad != 0u; bad &= bad - 1u) {
+    const int key = __ffs(bad) - 1;
+    const uint8_t* const codes = values + S::place(key, chunk);
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if ((codes[i] & 0x7fu) == 0x7fu) bits |= 1u << i;
+#pragma unroll 1
+    for (int r = 0; r < kWarpRows; ++r) {
+      const int32_t seen = __shfl_sync(0xffffffffu, len, r);
+      if (bits != 0u && lane < S::kChunks && j0 + key < seen) atomicOr(columns + r * (kDim / 32) + chunk / 2, bits << (chunk & 1) * 16);
+    }
+  }
+}
+
 // kTiles: tiles of 8 query rows of a warp. kRowWarps: warps that share keys.
 template <int kDim, int kTiles, int kRowWarps> struct Layout {
   using S = Shape<kDim>;
@@ -130,7 +158,8 @@ template <int kDim, int kTiles, int kRowWarps> struct Layout {
   static constexpr int kStatBytes = kWarps * kWarpRows * 8;
   static constexpr int kRowFloats = kDim + 4;                            // four rows two apart lie 8 banks from each other
   static constexpr int kSumBytes = kSent * kRows * kRowFloats * 4;
-  static constexpr int kRest = kQueryBytes + kFactorBytes + kStatBytes + kSumBytes;
+  static constexpr int kColumnBytes = kRows * kDim / 8;
+  static constexpr int kRest = kQueryBytes + kFactorBytes + kStatBytes + kSumBytes + kColumnBytes;
   static constexpr int kFit = (kMaxShared / kCtas - kRest) / (kKeyWarps * S::kStageBytes);
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static_assert(kStages >= 3, "stages ahead");
@@ -138,8 +167,9 @@ template <int kDim, int kTiles, int kRowWarps> struct Layout {
   static constexpr int kQuery = kKeyWarps * kRing;                       // then the queries' operands,
   static constexpr int kFactor = kQuery + kQueryBytes;                   // the factor of each row,
   static constexpr int kStats = kFactor + kFactorBytes;                  // bound and sum of each row and warp,
-  static constexpr int kSums = kStats + kStatBytes;                      // and warps' sums
-  static constexpr int kBytes = kSums + kSumBytes;
+  static constexpr int kSums = kStats + kStatBytes;                      // warps' sums,
+  static constexpr int kColumns = kSums + kSumBytes;                     // and each row's columns that are NaN
+  static constexpr int kBytes = kColumns + kColumnBytes;
   static constexpr int64_t kPartial = kRows * (kDim + 2);                // floats of a piece in the workspace
 };
 
@@ -155,6 +185,7 @@ __global__ void __launch_bounds__(Layout<kDim, kTiles, kRowWarps>::kThreads, Lay
   // columns that the cache does not have are zeros, which no copy touches
   if (p.dim < kDim)
     for (int i = threadIdx.x; i < L::kQuery / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < L::kColumnBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(smem + L::kColumns)[i] = 0u;
   begin_after_prior_grids();
   find_span<L::kRows, L::kKeys>(p, sums, span);
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{span.total, 0, 0, 0, 0};
@@ -425,11 +456,10 @@ __global__ void __launch_bounds__(Layout<kDim, kTiles, kRowWarps>::kThreads, Lay
 #pragma unroll
           for (int e = 0; e < 2; ++e) s[t][2 * h + e] = fmaf(s[t][2 * h + e], sk * factor[t][e], more[h]);
       }
-      bool scrub = false;
+      uint32_t bad = 0;
       if (!whole) {
         // Where some rows see a key and others do not, a NaN among its value's codes would reach all of them through a
-        // weight of 0: there it becomes a NaN logit of the rows that see it, and 0.
-        uint32_t bad = 0;
+        // weight of 0: there it counts as 0, and the rows that see it are marked.
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           bool found = false;
@@ -443,18 +473,16 @@ __global__ void __launch_bounds__(Layout<kDim, kTiles, kRowWarps>::kThreads, Lay
           for (int q = 0; q < 4; ++q)
             if ((lanes & (0x11111111u << q)) != 0u) bad |= 1u << ((k >> 1) * 8 + 2 * q + (k & 1));
         }
-        scrub = bad != 0u;
+        bad |= (bad & present) << 16;  // above: those that some row may see
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int key = g + 8 * h;
-          const bool there = (present >> key & 1u) != 0u, nan = (bad >> key & 1u) != 0u;
+          const bool there = (present >> key & 1u) != 0u;
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e)
               if (!there || j0 + key >= len[t][e]) s[t][2 * h + e] = none;
-              else if (nan) s[t][2 * h + e] = __uint_as_float(0x7fffffffu);
-            }
         }
       }
       // ---- weights
@@ -501,8 +529,13 @@ __global__ void __launch_bounds__(Layout<kDim, kTiles, kRowWarps>::kThreads, Lay
         }
       }
       // ---- values . weights
-      if (scrub) weigh<kDim, kTiles, true>(o, weights, values, g, c);
-      else weigh<kDim, kTiles, false>(o, weights, values, g, c);
+      if (bad != 0u) {
+        weigh<kDim, kTiles, true>(o, weights, values, g, c);
+        mark<kDim, L::kWarpRows>(p, reinterpret_cast<uint32_t*>(smem + L::kColumns) + mw * L::kWarpRows * (kDim / 32), bad >> 16, values, j0,
+                                 use.list, r0 + mw * L::kWarpRows);
+      } else {
+        weigh<kDim, kTiles, false>(o, weights, values, g, c);
+      }
     }
 
     // ---- the end of the tile, or of the span: the warps along the keys, joined in a fixed order
@@ -565,6 +598,31 @@ __global__ void __launch_bounds__(Layout<kDim, kTiles, kRowWarps>::kThreads, Lay
       if (rest > 1) __syncthreads();
     }
     if (kw == 0) {
+      uint32_t* const columns = reinterpret_cast<uint32_t*>(smem + L::kColumns) + mw * L::kWarpRows * (kDim / 32);
+      uint32_t spoiled[kTiles][2][(kDim + 127) / 128], any = 0;  // of this lane's columns: neighbouring bits
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < (kDim + 127) / 128; ++i) {
+            const int col = S::column(8 * i, g, 0);
+            spoiled[t][e][i] = columns[(t * 8 + 2 * c + e) * (kDim / 32) + col / 32] >> (col % 32);
+            any |= spoiled[t][e][i];
+          }
+      if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int m = 0; m < S::kOut; ++m) {
+              const uint32_t two = spoiled[t][e][m / 8] >> (2 * (m % 8));
+              if ((two & 1u) != 0u) o[m][t][e] = __uint_as_float(0x7fffffffu);
+              if ((two & 2u) != 0u) o[m][t][2 + e] = __uint_as_float(0x7fffffffu);
+            }
+        for (int i = lane; i < L::kWarpRows * (kDim / 32); i += 32) columns[i] = 0u;  // (all of the warp have read theirs)
+      }
       if (from_start && to_end) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)

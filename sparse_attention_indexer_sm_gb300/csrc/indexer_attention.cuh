@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const bool any = part.y != -1.0f;  // a sum of weights is not negative
     const float f = part.x == none ? 1.0f : exp2_fast(part.x - top);
     total += any ? part.y * f : 0.0f;
-    part.x = any ? f : 0.0f;
+    part.x = any ? f : -1.0f;  // (a share may round to 0: a NaN among its piece's sums still counts)
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll 4
     for (int32_t k = 0; k < pieces; ++k) {
       const float f = parts[k * kJoinRows + r].x;
-      if (f != 0.0f) {  // else there is nothing, or nothing that counts
+      if (f >= 0.0f) {  // else there is no piece
         const float4 v = *reinterpret_cast<const float4*>(base + (2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0)) * floats);
         sum[0] = fmaf(v.x, f, sum[0]), sum[1] = fmaf(v.y, f, sum[1]), sum[2] = fmaf(v.z, f, sum[2]), sum[3] = fmaf(v.w, f, sum[3]);
       }

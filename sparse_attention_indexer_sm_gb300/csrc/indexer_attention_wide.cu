@@ -92,6 +92,8 @@ template <int kParts, int kTileRows> struct Shared {
   alignas(16) float key_scales[kValueStages][kTile], logs[kValueStages][kTile], inverses[kValueStages][kTile];
   alignas(16) uint32_t present[kValueStages][4];
   uint32_t uniform[kValueStages][4];                           // 32 keys there and with the same scales
+  uint32_t clean[kValueStages][4];                             // keys there without a NaN among their value's codes
+  alignas(16) uint32_t nan_columns[2][kTile][4];               // of rows that see such a key: see mark_columns
   float factors[4][2 * kTile];  // of four items: read until an item's last weights are made
   float2 stats[2][2][kTile];
   float joined[P::kSpread > 1 ? kTile : 1][kJoinWidth];        // 32 columns of the sums that make a row
@@ -373,6 +375,15 @@ __device__ __forceinline__ void multiply(const AttendParams& p, Shared<kParts, k
 
 // ---------------------------------------------------------------- the loaders
 
+// The fp16 number that stands for a NaN code among the values: the largest one, no code's. A row that does not see the key adds it
+// with a weight of 0; of a row that does, the column becomes NaN at the item's end.
+constexpr uint32_t kNanMark = 0x7bffu;
+// Two values that were codes, with the mark for each NaN (all bits below the sign).
+__device__ __forceinline__ uint32_t marked(uint32_t two) {
+  const uint32_t nan = ((two & 0x7fff7fffu) + 0x00010001u) & 0x80008000u;
+  return two & ~(nan | nan >> 5);
+}
+
 // 16 bytes that leave no line in L1, of which shared memory leaves little (a prompt's chunk 374 -> 360 us).
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 v;
@@ -524,21 +535,21 @@ __device__ __forceinline__ void load(const AttendParams& p, Shared<kParts, kTile
       arrive(&s.key_full[key]);
       // ---- values become fp16
       if (ring.value_use > 0) wait(&s.value_empty[stage], ring.value_use - 1);
-      uint32_t bad = 0;  // rows with a NaN code: it becomes 0, for the rows that do not see it, and a NaN logit for those that do
+      uint32_t bad = 0;  // rows with a NaN code: it becomes kNanMark, which is no code's value and adds 0 where the key is not seen
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         uint32_t x[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
         const bool nan = ((nan_codes(x[0]) | nan_codes(x[1])) | (nan_codes(x[2]) | nan_codes(x[3]))) != 0u;
         const uint32_t lanes = __ballot_sync(0xffffffffu, nan);
+        uint4 first = make_uint4(halves_of(x[0]), halves_of(x[0] >> 16), halves_of(x[1]), halves_of(x[1] >> 16));
+        uint4 second = make_uint4(halves_of(x[2]), halves_of(x[2] >> 16), halves_of(x[3]), halves_of(x[3] >> 16));
         if (lanes != 0u) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            x[w] &= ~((nan_codes(x[w]) >> 7) * 0xffu);
+          for (int w = 0; w < 4; ++w)
             if ((lanes >> (8 * w) & 0xffu) != 0u) bad |= 1u << (4 * k + w);
-          }
+          first = make_uint4(marked(first.x), marked(first.y), marked(first.z), marked(first.w));
+          second = make_uint4(marked(second.x), marked(second.y), marked(second.z), marked(second.w));
         }
-        const uint4 first = make_uint4(halves_of(x[0]), halves_of(x[0] >> 16), halves_of(x[1]), halves_of(x[1] >> 16));
-        const uint4 second = make_uint4(halves_of(x[2]), halves_of(x[2] >> 16), halves_of(x[3]), halves_of(x[3] >> 16));
         // eight lanes store eight pieces of different banks: the lanes of the other block begin with their second piece
         const int row = key0 + row0 + 4 * k, odd = chunk >> 2, at = 2 * (chunk & 3);
         uint8_t* const to = s.values[stage][chunk >> 2] + row * 128;
@@ -547,14 +558,15 @@ __device__ __forceinline__ void load(const AttendParams& p, Shared<kParts, kTile
       }
       const float scale = max_or_nan(scales[1], 0x1p-100f);  // no logarithm of zero
       s.key_scales[stage][key0 + lane] = scales[0];
-      s.logs[stage][key0 + lane] = (bad >> lane & 1u) != 0u ? __uint_as_float(0x7fffffffu) : log2_fast(scale);
+      s.logs[stage][key0 + lane] = log2_fast(scale);
       s.inverses[stage][key0 + lane] = inverse_fast(scale);
       int same_keys, same_values;
       __match_all_sync(0xffffffffu, __float_as_uint(scales[0]), &same_keys);
       __match_all_sync(0xffffffffu, __float_as_uint(scales[1]), &same_values);
       if (lane == 0) {
         s.present[stage][key0 / 32] = present;
-        s.uniform[stage][key0 / 32] = same_keys != 0 && same_values != 0 && present == 0xffffffffu && bad == 0u ? 1u : 0u;
+        s.clean[stage][key0 / 32] = present & ~bad;
+        s.uniform[stage][key0 / 32] = same_keys != 0 && same_values != 0 && present == 0xffffffffu ? 1u : 0u;
       }
       arrive(&s.value_full[stage]);
     }
@@ -563,6 +575,33 @@ __device__ __forceinline__ void load(const AttendParams& p, Shared<kParts, kTile
 }
 
 // ---------------------------------------------------------------- the softmax
+
+// Adds to `columns` (128 bits of this thread's row) those of its value that a NaN code has, for each of 32 keys (key0 on, of the
+// tile) that `bad` names and the row sees: the first `seen` of them. All of a warp's threads read the same values. A call, out of the
+// loop's way (64 sequences of up to 8192 keys, 64 query heads on each of 8: 287 us in the loop, 281 so).
+__device__ __noinline__ void mark_columns(uint32_t* columns, const uint8_t* values, uint32_t bad, int key0, int32_t seen) {
+#pragma unroll 1
+  for (; bad != 0u; bad &= bad - 1u) {
+    const int key = __ffs(bad) - 1, row = key0 + key;
+#pragma unroll 1
+    for (int word = 0; word < kDim / 32; ++word) {
+      uint32_t bits = 0;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {  // 8 columns
+        const int piece = 4 * (word & 1) + k;
+        const uint4 v = *reinterpret_cast<const uint4*>(values + (word >> 1) * (kTile * 128) + row * 128 + ((piece ^ (row & 7)) * 16));
+        const uint32_t two[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bits |= (two[i] & 0xffffu) == kNanMark ? 1u << (8 * k + 2 * i) : 0u;
+          bits |= two[i] >> 16 == kNanMark ? 1u << (8 * k + 2 * i + 1) : 0u;
+        }
+      }
+      if (bits != 0u && key < seen) atomicOr(columns + word, bits);  // (both streams' threads of a row, or its two lanes)
+    }
+  }
+  __syncwarp();
+}
 
 // N values of a row of the output, from column `col` on.
 template <int N>
@@ -635,9 +674,9 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
             const int32_t j0 = (it.first + t) * kTile + at;
             float x[32];
             tmem_load(logits + at, x);
-            const uint32_t present = s.present[stage][at / 32];
+            const uint32_t clean = s.clean[stage][at / 32];
             const bool uniform = s.uniform[stage][at / 32] != 0u;  // all with the same scales: what they add is worked out once
-            const bool whole = __all_sync(0xffffffffu, present == 0xffffffffu && j0 + 32 <= len);
+            bool whole = __all_sync(0xffffffffu, clean == 0xffffffffu && j0 + 32 <= len);
             const float base = bound == none ? 0.0f : bound - kShift;
             const float4* const ks = reinterpret_cast<const float4*>(&s.key_scales[stage][at]);
             const float4* const lg = reinterpret_cast<const float4*>(&s.logs[stage][at]);
@@ -663,6 +702,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
               }
             }
             if (!whole) {
+              const uint32_t present = s.present[stage][at / 32];
+              if (present != clean) {
+                mark_columns(s.nan_columns[kPair ? st : items & 1][kPair ? m : r], s.values[stage][0], present & ~clean, at,
+                             used ? len - j0 : 0);
+                whole = __all_sync(0xffffffffu, present == 0xffffffffu && j0 + 32 <= len);  // the sums' order goes by what is seen
+              }
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if ((present >> k & 1u) == 0u || j0 + k >= len) x[k] = none;
@@ -782,6 +827,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
           *reinterpret_cast<float4*>(piece + static_cast<int64_t>(r) * kDim + k + i) = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
       }
     };
+    auto spoil = [&](auto& v, uint32_t columns) {
+      if (columns == 0u) return;
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(v) / sizeof(float)); ++i)
+        if ((columns >> i & 1u) != 0u) v[i] = nan;
+    };
     auto put_stats = [&](float top, float total) {
       if (!used) return;
       if (!alone) *reinterpret_cast<float2*>(piece + P::kRows * kDim + 2 * r) = make_float2(top, total);
@@ -800,9 +851,11 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
           float o[32];
           tmem_load(sums + k, o);
           tmem_wait(o);
+          spoil(o, s.nan_columns[st][m][k / 32]);
           put_row(k, o, f);
         }
       }
+      *reinterpret_cast<uint4*>(s.nan_columns[st][m]) = make_uint4(0, 0, 0, 0);
       tmem_fence_before();
       bar_arrive(&s.sums_empty[st]);
     } else if constexpr (kSpread > 1) {
@@ -856,9 +909,11 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
               const float4 v = *reinterpret_cast<const float4*>(&s.joined[from * P::kRows + r][share * kColumns + i]);
               y[i] += v.x, y[i + 1] += v.y, y[i + 2] += v.z, y[i + 3] += v.w;
             }
+          spoil(y, s.nan_columns[items & 1][r][k / 32] >> (share * kColumns));
           put_row(k + share * kColumns, y, out);
         }
         named_barrier<kTile>(4);
+        if (share == 0) *reinterpret_cast<uint4*>(s.nan_columns[items & 1][r]) = make_uint4(0, 0, 0, 0);
         tmem_fence_before();
         bar_arrive(&s.sums_empty[0]);
         bar_arrive(&s.sums_empty[1]);
@@ -894,9 +949,11 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
 #pragma unroll
               for (int i = 0; i < 32; ++i) a[i] = fmaf(b[i], f1, a[i]);
             }
+            spoil(a, s.nan_columns[items & 1][r][k / 32]);
             put_row(k, a, out);
           }
         }
+        *reinterpret_cast<uint4*>(s.nan_columns[items & 1][r]) = make_uint4(0, 0, 0, 0);  // for the item after the next one
         tmem_fence_before();
         bar_arrive(&s.sums_empty[0]);
         bar_arrive(&s.sums_empty[1]);
@@ -939,6 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     s.aborted = p.fail;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x < 2 * kTile) *reinterpret_cast<uint4*>(s.nan_columns[threadIdx.x / kTile][threadIdx.x % kTile]) = make_uint4(0, 0, 0, 0);
   // columns that the cache does not have are zeros, which no copy touches
   if (p.dim < kDim)
     for (int i = threadIdx.x; i < P::kKeyStages * kTile * kDim / 16; i += kThreads) reinterpret_cast<uint4*>(s.keys)[i] = make_uint4(0, 0, 0, 0);

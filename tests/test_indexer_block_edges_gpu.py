@@ -9,7 +9,8 @@ import math
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_indexer_attention_gpu import append_ref, make_cache, same  # noqa: E402
+from test_indexer_attention_gpu import (  # noqa: E402
+    MANY, append_ref, attention_ref, ints, make_cache, make_case, same, slots_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -190,6 +191,85 @@ def test_attention_over_a_cache_without_pages(fw, group, dim, size):
     assert not out.any() and (lse == -math.inf).all()
     assert fw.indexer_guard_hits() >= 5
     fw.indexer_reset_guard_hits()
+
+
+NAN_CODES = [  # batch, queries, kv heads, group, dim, pages of a sequence, page size, block
+    (2, 3, 2, 2, 128, 60, 16, 16), (3, 1, 1, 8, 64, 40, 16, 4), (1, 2, 2, 9, 128, 50, 16, 16), (2, 1, 1, 30, 128, 30, 7, 7),
+    (1, 5, 1, 13, 64, 40, 16, 16), (2, 1, 2, 14, 256, 30, 16, 16), (1, 4, 1, 5, 192, 20, 5, 1), (2, 1, 2, 40, 128, 50, 16, 16),
+    (1, 9, 1, 7, 112, 60, 16, 2), (2, 1, 1, 100, 128, 40, 16, 16), (1, 50, 2, 4, 128, 30, 16, 16), (1, 130, 1, 2, 80, 40, 16, 16)]
+
+
+@pytest.mark.parametrize("softmax_scale", [0.1, 4.0])
+@pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("case", NAN_CODES)
+def test_attention_a_nan_code_of_a_value_stays_in_its_column(fw, case, dtype, softmax_scale):
+    """The formula's own result: that column of the queries that see the key is NaN, however little the key weighs, wherever the
+    work is cut and whatever other queries of the tile see; other columns, queries and the logarithm are as without it."""
+    batch, queries, kv, group, dim, width, size, block = case
+    g, q, k, v, table = make_case(sum(case) + 1, *case, dtype)
+    length = width * size
+    lens = (ints(g, length // 2, length + 1, (batch, 1)) - queries + 1 + torch.arange(queries)).int()
+    lens[0] += length - lens[0, -1]
+    clean = v[0].clone()
+    spoiled = v[0].view(torch.uint8)
+    for b in range(batch):  # a few keys anywhere, the first, and those around each query's last
+        at = torch.cat([torch.tensor([0]), torch.randint(0, length, (4,), generator=g), (lens[b, ::3].long() - 1), lens[b, -1:].long()])
+        for j in at.clamp(0, length - 1).tolist():
+            slot = int(slots_of(table[b], size, length)[j])
+            h, col = int(ints(g, 0, kv, ())), int(ints(g, 0, dim, ()))
+            spoiled[slot // size, slot % size, h, col] = 0x7f + 128 * (j % 2)
+            clean.view(torch.uint8)[slot // size, slot % size, h, col] = 0
+    nan = v[0].cpu().float().isnan().flatten(0, 1)
+
+    def compare(out, got, sees):
+        ref, tol, lse, lse_tol = attention_ref(q.flatten(0, 1), k, (clean, v[1]), sees, softmax_scale)
+        want = torch.stack([nan[sees(r)].any(0).repeat_interleave(group, 0) for r in range(batch * queries)])
+        out, got = out.double().cpu().flatten(0, 1), got.double().cpu().flatten(0, 1)
+        assert want.any() and torch.equal(out.isnan(), want)
+        eps = torch.finfo(dtype).eps
+        bound = tol + (ref.abs() + tol) * eps / 2 + torch.finfo(dtype).smallest_normal * eps
+        assert (((out - ref).abs() <= bound) | want).all()
+        assert ((got - lse).abs() <= lse_tol).all()
+
+    args = dict(softmax_scale=softmax_scale, return_lse=True)
+    whole = lambda r: slots_of(table[r // queries], size, int(lens[r // queries, r % queries]))  # noqa: E731
+    compare(*fw.indexer_attention(q, *k, *v, page_table=table.cuda(), seq_lens=lens.cuda(), **args), whole)
+    slots = torch.full((batch * queries, length), -1, dtype=torch.int32)
+    for r in range(batch * queries):  # the same rows as picks in another order, some places empty
+        mine = whole(r)
+        slots[r, torch.randperm(length, generator=g)[:len(mine)]] = mine.int()
+    compare(*fw.indexer_attention(q, *k, *v, slots=slots.cuda(), **args), lambda r: slots[r][slots[r] >= 0].long())
+
+
+@pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("case", MANY + [(300, 1, 2, 8, 128, 4, 16, 16), (200, 1, 1, 30, 128, 5, 16, 16), (200, 2, 1, 16, 64, 5, 7, 7)])
+def test_attention_nan_codes_in_many_tiles_of_a_cta(fw, case, dtype):
+    """To the last bit what the same call gives with 0 in their place, but for NaN in these columns of the queries that see them:
+    nothing goes from one tile of a CTA to the next ones. In every run."""
+    batch, queries, kv, group, dim, width, size, block = case
+    g, q, k, v, table = make_case(sum(case) + 2, *case, dtype)
+    length = width * size
+    lens = (ints(g, 0, length + 1, (batch, 1)) - queries + 1 + torch.arange(queries)).int()
+    args = dict(page_table=table.cuda(), seq_lens=lens.cuda(), return_lse=True)
+    codes = v[0].view(torch.uint8)
+    place = torch.rand((batch, length), generator=g) < 1.5 / length  # one or two of a sequence's keys, many sequences none
+    place[::3] = False
+    want = torch.zeros((batch, queries, kv, dim), dtype=torch.bool)
+    put = []
+    for b, j in place.nonzero().tolist():
+        slot, h, col = int(slots_of(table[b], size, length)[j]), int(ints(g, 0, kv, ())), int(ints(g, 0, dim, ()))
+        put.append((slot // size, slot % size, h, col))
+        want[b, :, h, col] |= lens[b] > j
+    at = tuple(torch.tensor(i).cuda() for i in zip(*put))
+    codes[at] = 0
+    out, lse = fw.indexer_attention(q, *k, *v, **args)
+    codes[at] = 0xff
+    assert want.any()
+    want = out.masked_fill(want.repeat_interleave(group, 2).cuda(), math.nan)
+    for _ in range(20):
+        got, other = fw.indexer_attention(q, *k, *v, **args)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+        assert torch.equal(other, lse)
 
 
 # ---------------------------------------------------------------- captured gradients
