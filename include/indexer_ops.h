@@ -235,7 +235,9 @@ int indexer_cache_append(const void* x, int64_t x_token_stride, int64_t x_head_s
                          int32_t batch, const indexer_block_cache_t* cache, cudaStream_t stream);
 
 /* Attention over block-scaled caches of keys and values (as many pages, page_size, heads and
- * dim in both). q [batch, queries, heads, dim] of `dtype` (bf16 or fp16), contiguous, 16-byte
+ * dim in both, heads of INDEXER_MAX_HEAD_DIM columns at most: not rows of an indexer_cache_t, with
+ * a scale for each 128 columns, nor one latent row that is key and value at once; read such rows
+ * back with indexer_cache_read). q [batch, queries, heads, dim] of `dtype` (bf16 or fp16), contiguous, 16-byte
  * aligned, heads a multiple of the caches' (query head h reads their head
  * h / (heads / cache heads)); out like q. For query (b, n) and the set J of positions it sees:
  *   out = sum_J p_j v_j / sum_J p_j,  p_j = exp(softmax_scale * q . k_j)
@@ -248,10 +250,14 @@ int indexer_cache_append(const void* x, int64_t x_token_stride, int64_t x_head_s
  * slot that is there twice counts twice. A page id or slot outside the cache: its
  * positions are left out, and it is counted.
  * Values of q count to within 2^-17 of their row's largest one (or of 2^-112, where that is
- * larger); products with codes are exact, sums and the softmax in fp32; the weights p_j (with
- * the values' scales) are rounded to 11 bits for their products with the values' codes. The
- * split of the work depends on the sizes, the lengths and the device: the same call gives the
- * same bits, another batch around a query may change its last ones.
+ * larger); products with codes are exact, sums and the softmax in fp32. For their products with
+ * the values' codes the weights p_j (with the values' scales) are rounded to 11 bits, or to 2^-32
+ * of the row's largest one where that is coarser; from 65 query rows on a head of the cache on
+ * (heads of 80 to 128 columns) some are rounded so twice. A key whose p_j * scale lies below
+ * 2^-133 of the row's largest adds to neither sum: values' scales that lie within 2^100 of each
+ * other lose none that counts. The split of the work depends on the sizes, the lengths and the
+ * device: the same call gives the same bits, another batch around a query may change its last
+ * ones.
  * Scales of values are taken as at least 2^-100 (a negative one too), and keys that no query
  * sees may hold anything. For the queries that see the key, a NaN code of a value makes its
  * column NaN, however little the key weighs, and nothing else; a NaN among a key's codes or the

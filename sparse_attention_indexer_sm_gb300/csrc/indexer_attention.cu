@@ -20,11 +20,14 @@
 //   stages of 16 keys and values, which cp.async fills some steps ahead and across the ends of tiles. CTAs
 //   take equal spans of all the steps of all tiles, which each finds by adding up the lengths. A tile cut by a span's end
 //   leaves its unscaled sums, bounds and sums of weights in the workspace; a second kernel joins these, in order.
-// What bounds it: one query row, or a few, read the keys at 71% of the copy rate (64 sequences of up to 32768 keys of 8
-// heads, 8 query heads on each, 2.1 GB: 441 us). From 9 rows on it is the instructions of a step, 1050 for 32 rows on 16
+// What bounds it: one query row, or a few, read the keys at 73% of the copy rate (64 sequences of up to 32768 keys of 8
+// heads, 8 query heads on each, 1054085 keys and 2.16 GB in all: 435 us). From 9 rows on it is the instructions of a step, 1050 for 32 rows on 16
 // keys, of which conversions of the codes and the products' operands are most: 256 rows of 2048 picks, 2 heads, 32 query
-// heads on each (270 MB) take 134 us. Picked rows of 128 bytes arrive at 4.5 TB/s at best (a kernel of copies alone). The
+// heads on each (270 MB) take 135 us. Picked rows of 128 bytes arrive at 4.5 TB/s at best (a kernel of copies alone). The
 // codes as e4m3 operands of the logits' products, with queries in parts, cost more than they save (134 -> 168 us).
+// Heads of 64 columns, and of more than 128, take these tiles at any number of query rows, and are far from their floor with many: a
+// prompt's chunk of 1024 queries behind 15360 keys, 8 heads, 4 query heads on each, 1171 us with 64 columns and 2741 with 256, for
+// 70 and 281 us of products.
 
 #include <algorithm>
 
@@ -720,8 +723,8 @@ cudaError_t run_rows(const AttendParams& p, int sms, cudaStream_t stream) {
 }
 
 // More query rows on the same keys than two warps of a tile: the kernel of wide tiles, whose rows have 128 columns (64
-// sequences of up to 8192 keys of 8 heads, 40 query heads on each: 283 us there, 323 in tiles of three warps; 32 query heads:
-// 241 in tiles of two warps, 299 there).
+// sequences of up to 8192 keys of 8 heads, 40 query heads on each: 279 us there, 323 in tiles of three warps; 32 query heads:
+// 248 in tiles of two warps, 299 there).
 bool wide_tile(int64_t rows, int32_t dim) { return padded_dim(dim) == 128 && rows > 32; }
 
 cudaError_t run_attention(const AttendParams& p, int sms, cudaStream_t stream) {

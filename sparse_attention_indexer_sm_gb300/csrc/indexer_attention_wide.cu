@@ -3,8 +3,9 @@
 //
 // Both products run on tcgen05 with query rows as the 128 lanes of TMEM:
 // - q . k: the keys' codes are an operand as they are (kind::f8f6f4). A query row, scaled by a power of two that brings its
-//   largest value to [2^7, 2^8), is the sum of two (bf16) or three (fp16) e4m3 numbers: all its bits down to 2^-9 of the
-//   largest value, and to within 2^-17 of it below. Sums are in fp32; the products of the parts add up in TMEM.
+//   largest value to [2^7, 2^8), is the sum of two (bf16) or three (fp16) e4m3 numbers: all bits of values down to 2^-9 (bf16) or
+//   2^-6 (fp16) of 2^7, where e4m3's last step, 2^-9, is their own last bit, and to within 2^-17 of the largest value below. Sums
+//   are in fp32; the products of the parts add up in TMEM.
 // - weights . v: the weights are fp16, in TMEM over the logits that they come from; the values' codes become fp16 in
 //   shared memory, as many bits as they have. The tensor cores would take their codes too, but weights of 4 bits lose what many
 //   small ones add up to.
@@ -18,12 +19,14 @@
 // With more than 128 rows the streams are two tiles of rows on the same keys. With fewer they are one tile on every
 // second tile of 128 keys each, and are joined at the tile's end. Of 64 rows and fewer each has two of a stream's lanes, with
 // 32 keys of a half each and weights of zero for the other's (64 sequences of up to 8192 keys, 64 query heads on each of 8: 289 us
-// when it was taken, 324 with one lane and half of the softmax threads without work; 280 now).
+// when it was taken, 324 with one lane and half of the softmax threads without work; 278 now).
 // What bounds it: a prompt's chunk (1024 queries behind 15360 keys, 8 heads, 4 query heads on each; 140 us of products at the
-// measured rate) takes 353 us, most of it the softmax's instructions: 128 threads a stream, 32 logits each at a time. Few
-// rows wait for the loaders, 8 warps that send copies, wait, and convert: 16 sequences of up to 16384 keys, 35 rows on each of 4
-// heads, 67 us. Copies sent a tile ahead held up the softmax's own loads behind them in the queue (100 us), with values' codes
-// in registers or by way of shared memory.
+// measured rate) takes 359 us. No pipe is full: of a smaller chunk 37% of the issue slots are taken, the tensor pipe is busy 24%
+// of the time, ALU 27%, exponentials 12%. Eight softmax warps, two a scheduler, each wait for their own logits from TMEM, compute,
+// store weights and wait for the store, 32 logits at a time, with nothing of the next ones under way. Few rows wait for the loaders
+// too, 8 warps that send copies, wait, and convert: 16 sequences of up to 16384 keys, 35 rows on each of 4 heads, 68 us. Copies
+// sent a tile ahead held up the softmax's own loads behind them in the queue (100 us), with values' codes in registers or by way
+// of shared memory.
 // Every wait has a limit (2.6 s in all); after it the roles run through to their end, in bounds, and give NaN.
 
 #include <algorithm>
@@ -46,7 +49,7 @@ constexpr int kTmemColumns = 512;
 constexpr int kWaitLimit = 1 << 17;      // tries of a wait before it is given up,
 constexpr uint32_t kWaitNs = 20000;      // each of which may sleep this long: 2.6 s in all
 // Registers of a thread: of the 640 * 96 of a launch, 256 * 120 + 256 * 96 + 128 * 40 = 60416; the loaders keep theirs (a
-// prompt's chunk 353 us; with 136 and 80 365, with 104 and 112 363).
+// prompt's chunk 353 us when they were taken; with 136 and 80 365, with 104 and 112 363).
 constexpr int kSoftmaxRegisters = 120, kOtherRegisters = 40;
 
 constexpr int kJoinWidth = 36;           // eight lanes' pieces on different banks
@@ -725,7 +728,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, Shared<kParts, kT
 #pragma unroll
               for (int k = 0; k < 32; ++k) x[k] -= down;
               sum2 = mul2(sum2, pack2(f, f));
-              if (c > 0) {  // the half's weights so far, which are no part of the sums yet
+              if (c > 0) {  // the half's weights so far, which are no part of the sums yet: rounded to 11 bits once more
                 tmem_stored();
                 float y[32];  // (the second 16 columns are logits, and stay)
                 tmem_load(weights, y);

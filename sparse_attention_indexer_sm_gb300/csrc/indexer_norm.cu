@@ -12,10 +12,14 @@
 // - The parameters' gradients. A lane holds the same columns of all of its rows, so a CTA, which walks over many rows,
 //   adds up both sums in registers, joins its groups once at its end in a fixed order, and leaves one row of partial
 //   sums; a second kernel adds those up. No atomics: the same sums in every run.
-// Measured, forward and all gradients together, in a graph: 16384 rows of 1536 in bf16 67 us (252 MB: 37 us at the copy
-// rate), 131071 rows of 128 43 us (25); a decode step's 48 rows of 128, forward, 1.6 us. The gradient's loads wait for a
-// row's two sums between them. Two rows at once (57 us), the next row's loads ahead of this one's sums (62 and 35 us for the
-// gradients alone) and a CTA or a warp for each wide row were slower: their registers cost as many resident warps.
+// Measured in bf16, in a graph: 131071 rows of 128, forward 15.5 us (10 at the copy rate), with all gradients 44 (25); 16384
+// rows of 1536 23.5 (15) and 68 (37); a decode step's 48 rows of 128, forward, 1.5. What bounds it is instructions as much as
+// loads: of narrow rows the forward has 3.0 issued a clock and SM (of four), the ALU busy half of the time, the gradient 2.4, and
+// each row's loads come before its two sums, with nothing of the next row under way. Two rows at once (57 us), the next row's loads
+// ahead of this one's sums (62 and 35 us for the gradients alone) and a CTA or a warp for each wide row were slower: their registers
+// cost as many resident warps. Rows on no 16-byte boundary are read a value at a time: 16384 rows of 1002 31 and 91 us (of 1000: 18
+// and 53), of 1537, which no group holds, 69 and 249; long rows are read three times, and twice more for the parameters'
+// gradients: 4096 rows of 16384 133 us (40) and 631 (99).
 
 #include <algorithm>
 

@@ -386,7 +386,13 @@ def indexer_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Te
     counted (indexer_guard_hits). softmax_scale: dim ** -0.5 where None. Returns the output, of
     q's shape and type; with return_lse (output, fp32 [batch, queries, heads]), the logarithm of
     the sum of exponentials (-inf for a query that sees nothing), to join outputs over several
-    caches. There is no gradient, as in indexer_quantise."""
+    caches. A NaN code of a value makes its column NaN for the queries that see it; a NaN among a
+    key's codes or the scales makes their whole rows NaN. There is no gradient, as in
+    indexer_quantise.
+
+    Heads have at most 256 columns, and keys and values rows of their own: the rows of
+    indexer_cache_write (one wide latent row for keys and values, with a scale for each 128
+    columns) are read back by indexer_cache_read, not attended to here."""
     f = (_binding or _load_binding()).attention
     args = (q, k_codes, k_scales, v_codes, v_scales, page_table, seq_lens, slots, softmax_scale, return_lse, out)
     y, lse = _on(stream, f, *args) if stream is not None else f(*args, None)
